@@ -88,7 +88,8 @@ typedef enum {
   TV_ERR_BAD_TREE = 3,    /* device: parent[] not topological or node_offsets invalid   */
   TV_ERR_BAD_PATH = 4,    /* device: accepted_path not a root-first chain of the tree   */
   TV_ERR_CUDA = 5,        /* a CUDA runtime call failed (launch, copy, attribute)       */
-  TV_ERR_TIMEOUT = 6      /* device: a bounded wait in a kernel ran out; outputs invalid */
+  TV_ERR_TIMEOUT = 6,     /* device: a bounded wait in a kernel ran out; outputs invalid */
+  TV_ERR_BAD_PARAM = 7    /* device: a sampling parameter outside its range             */
 } tv_status;
 
 typedef enum { TV_MODE_GDN = 0, TV_MODE_SCALAR_DECAY = 1 } tv_mode;
@@ -256,6 +257,101 @@ TV_API tv_status tv_snapshot_commit(const tv_problem *p, const float *snapshots,
                                     const int32_t *accepted_path, const int32_t *parent,
                                     float *S_new, void *workspace, size_t workspace_bytes,
                                     tv_stream_t stream);
+
+/* ---- around the verification: prompts, single tokens, sampling, acceptance -------------
+ * A decode loop is  tv_prefill (the prompt's state), then per step  tv_tree_verify,  the
+ * model's logits,  tv_sample (one target token per node),  tv_tree_accept  and
+ * tv_tree_commit;  tv_decode_step  takes the place of a tree for sequences without a draft.
+ * The conventions above hold.  The recurrence is fp32 throughout: the states that these
+ * entry points write are within a few 1e-7 of the exact ones (relative, 2-norm), and out is
+ * rounded once to its type.  For a decay below exp(-1000) the result is that of a decay of
+ * zero, so log_a = -inf starts a state afresh. */
+
+/* The recurrence over whole prompts: for every token t of a sequence, in order,
+ *   S_t as above from S_{t-1},  out_t = S_t q_t,
+ * from S_in to S_out.
+ *   p          B, H, dk, dv, mode, in_dtype, out_dtype, kernel, qk_heads as for trees;
+ *              total_nodes = T, the rows of q, k, v, out; max_nodes = an upper bound on any
+ *              sequence's length (any, 0 too); max_path and u_dtype are not used
+ *   q, k       [T][Hk][dk] in_dtype; v [T][H][dv] in_dtype; log_a, b [T][H] fp32 (b may be
+ *              NULL in scalar mode)                                    (device, read)
+ *   seq_offsets [B+1] int32: sequence s owns rows seq_offsets[s] .. seq_offsets[s+1]-1.  The
+ *              last may end before T: rows that no sequence owns are neither read nor written.
+ *              An empty sequence keeps its state                       (device, read)
+ *   S_in       [B][H][dv][dk] fp32, or NULL for zero states             (device, read)
+ *   out        [T][H][dv] out_dtype                                     (device, written)
+ *   S_out      [B][H][dv][dk] fp32; may be S_in itself, must not partially overlap it
+ *                                                                       (device, written)
+ *   workspace  tv_prefill_workspace_size(p) bytes, as for trees.  Calls that may run at the
+ *              same time need a workspace each.
+ * A sequence whose range is not inside [0, T] or is longer than max_nodes records
+ * TV_ERR_BAD_TREE and is left unwritten. */
+TV_API size_t tv_prefill_workspace_size(const tv_problem *p);
+TV_API tv_status tv_prefill(const tv_problem *p, const void *q, const void *k, const void *v,
+                            const float *log_a, const float *b, const int32_t *seq_offsets,
+                            const float *S_in, void *out, float *S_out, void *workspace,
+                            size_t workspace_bytes, tv_stream_t stream);
+
+/* The recurrence for one token of every sequence: row s of q, k [B][Hk][dk], v, out [B][H][dv],
+ * log_a, b [B][H] belongs to sequence s (p->total_nodes = B).  S_new [B][H][dv][dk] may be S
+ * itself, must not partially overlap it.  Nothing in the data can be invalid, so there is no
+ * workspace. */
+TV_API tv_status tv_decode_step(const tv_problem *p, const void *q, const void *k, const void *v,
+                                const float *log_a, const float *b, const float *S, void *out,
+                                float *S_new, tv_stream_t stream);
+
+/* Logits to sample from: `rows` rows of `vocab` (1 .. 2^20) values, row r at
+ * logits + r * row_stride elements (row_stride >= vocab); in_dtype a tv_dtype. */
+typedef struct {
+  int32_t rows, vocab;
+  int64_t row_stride;
+  int32_t in_dtype, reserved;
+} tv_sample_problem;
+
+/* One token per row.  With m the row's largest logit, token i weighs exp((x_i - m) / t).
+ * In the order "larger logit first, lower index first among equals", the kept tokens are the
+ * shortest of these prefixes (one token at least):
+ *   top_k   the first top_k tokens (top_k <= 0 or >= vocab: all);
+ *   top_p   the tokens before which less than top_p of the mass of the top_k tokens lies
+ *           (1: all);
+ *   min_p   the tokens that weigh at least min_p (the largest weighs 1; 0: all).
+ * The token is the first in vocabulary order whose cumulated kept weight exceeds uniform
+ * times the kept total; weights and sums are in 64 bits.
+ *   logits      elements need only their own alignment                     (device, read)
+ *   uniform     [rows] fp32 in [0, 1], the random numbers                   (device, read)
+ *   temperature [rows] fp32, finite, >= 0 (0: the largest logit's token); NULL: 1
+ *   top_k       [rows] int32, NULL: all;  top_p, min_p [rows] fp32 in [0, 1], NULL: 1, 0
+ *   token       [rows] int32                                               (device, written)
+ *   logprob     [rows] fp32 or NULL: log of the probability that the token was drawn with
+ *               (kept weights, renormalised; 0 for temperature 0)           (device, written)
+ * NaN logits count as -inf, logits of -inf are never drawn; a row without any other gives
+ * token -1 and logprob -inf.  Where the largest logit is +inf, the tokens that have it share
+ * the weight.  A row with a parameter outside its range records TV_ERR_BAD_PARAM and is left
+ * unwritten.  workspace: tv_sample_workspace_size(p) bytes, as for trees; calls that may run
+ * at the same time need one each. */
+TV_API size_t tv_sample_workspace_size(const tv_sample_problem *p);
+TV_API tv_status tv_sample(const tv_sample_problem *p, const void *logits, const float *uniform,
+                           const float *temperature, const int32_t *top_k, const float *top_p,
+                           const float *min_p, int32_t *token, float *logprob, void *workspace,
+                           size_t workspace_bytes, tv_stream_t stream);
+
+/* The accepted path of every draft tree, for tv_tree_commit.  draft_token [T] is each node's
+ * proposed token, target_token [T] the token sampled after it, root_token [B] the one sampled
+ * after the committed state.  From the root, the lowest-index child whose draft token equals
+ * the target token of the current node (root_token at first) is accepted and becomes the
+ * current node, until there is none or max_path nodes are accepted.  Negative tokens match
+ * nothing.
+ *   accepted_path [B][max_path] root-first local indices, -1 padded        (device, written)
+ *   accepted_len  [B] accepted nodes;  next_token [B] the target token of the last accepted
+ *                 node (root_token if none)                                (device, written)
+ * p: B, total_nodes, max_nodes and max_path count; H, dk and dv only have to be valid.  A
+ * malformed tree records TV_ERR_BAD_TREE and its rows are left unwritten. */
+TV_API tv_status tv_tree_accept(const tv_problem *p, const int32_t *draft_token,
+                                const int32_t *target_token, const int32_t *root_token,
+                                const int32_t *parent, const int32_t *node_offsets,
+                                int32_t *accepted_path, int32_t *accepted_len,
+                                int32_t *next_token, void *workspace, size_t workspace_bytes,
+                                tv_stream_t stream);
 
 /* Diagnostic, with no counterpart on the pages: enqueue one small kernel whose bounded
  * wait on an mbarrier phase that never completes runs out.  It then records

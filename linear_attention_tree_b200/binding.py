@@ -28,14 +28,15 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtreeverify.so")
 
 TV_OK, TV_ERR_INVALID_ARG, TV_ERR_UNSUPPORTED, TV_ERR_BAD_TREE, TV_ERR_BAD_PATH, \
-    TV_ERR_CUDA, TV_ERR_TIMEOUT = range(7)
+    TV_ERR_CUDA, TV_ERR_TIMEOUT, TV_ERR_BAD_PARAM = range(8)
 MODE = {"gdn": 0, "scalar": 1}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 KERNEL = {"auto": 0, "tc": 1, "simt": 2}
 EXPORTS = ("tv_workspace_size", "tv_tree_verify", "tv_tree_commit", "tv_tree_meta",
            "tv_tree_commit_verify", "tv_snapshot_verify", "tv_snapshot_commit",
            "tv_get_status", "tv_status_string", "tv_last_cuda_error", "tv_version",
-           "tv_selftest_timeout")
+           "tv_selftest_timeout", "tv_prefill_workspace_size", "tv_prefill", "tv_decode_step",
+           "tv_sample_workspace_size", "tv_sample", "tv_tree_accept")
 
 
 class TreeVerifyError(RuntimeError):

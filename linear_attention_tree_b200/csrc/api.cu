@@ -59,7 +59,8 @@ tv_status record_cuda_error(cudaError_t e) { return from_cuda(e); }
 
 extern "C" {
 
-int32_t tv_version(void) { return (2 << 16) | 0; }   // 2: tv_problem gained u_dtype and qk_heads
+// 2: tv_problem gained u_dtype and qk_heads; 2.1: prefill, decode step, sampling, acceptance
+int32_t tv_version(void) { return (2 << 16) | 1; }
 
 const char *tv_last_cuda_error(void) {
   if (g_last_cuda == cudaSuccess) return "";
@@ -78,6 +79,7 @@ const char *tv_status_string(tv_status s) {
     case TV_ERR_BAD_PATH: return "bad accepted path";
     case TV_ERR_CUDA: return "CUDA runtime error";
     case TV_ERR_TIMEOUT: return "device wait timed out";
+    case TV_ERR_BAD_PARAM: return "bad sampling parameter";
   }
   return "unknown status";
 }
