@@ -7,11 +7,26 @@
 // token is the first in vocabulary order whose cumulated kept weight exceeds u times the total.
 // t = 0 keeps the largest logit alone.
 //
-// One CTA per row.  No sort: the two prefixes come from a radix descent over a monotone
-// 32-bit key of the logit, by count for top-k and by mass for top-p.  Masses that meet in
-// atomics are 64-bit integers (weight * 2^42), so their order does not matter; weights and
-// the sums that pick the token are in 64 bits, since a token is decided by where u * total
-// falls between two of up to a million borders.
+// Weights and the sums that decide a token are in 64 bits: a token is decided by where u * total
+// falls between two of up to a million borders, and 32-bit weights (1e-7 each) would put
+// one draw in some thousands on the wrong side.  The exponential is the cost (ten 64-bit
+// operations, half rate), so each row takes the way with the fewest of them:
+//   t = 0          the largest logit: one read of the row, no weight.
+//   small top-k    every thread keeps the largest logit of its stripe.  The k-th largest of
+//                  these 512 is at most the k-th largest logit, so the few logits above it hold
+//                  the prefix; only threads whose own maximum reaches it read their stripe
+//                  again.  What is left is a list of k to a few k tokens in shared memory.
+//   top-p          a second read sums all weights and counts tokens into 2048 bins of the
+//                  weight's logarithm, whose masses are known well enough (1e-4) to name the
+//                  bin of the border; a third read sums what lies above it by segments of the
+//                  vocabulary and lists the border's bins, where the border is found exactly.
+//                  Bins that hold more than the list are counted once more into 2048 parts of
+//                  their range of logits (for 16-bit logits, or such widened to 32: one part
+//                  per value, and the border is known), and a fourth read does the rest.
+//   otherwise      a second read sums the kept weights by segments.
+// The segment that holds the token is then read once more.  Where a list overflows or top-k is
+// large, the border comes from a radix descent over the logits' bits (slow and general).
+// Second and later reads hit L2.
 #include <math_constants.h>
 
 #include "serving.cuh"
@@ -21,215 +36,805 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kList = 1024;                    // candidates held in shared memory
+constexpr int kSmallK = 256;                   // largest top-k that goes by stripe maxima
+constexpr int kBins = 2048;
+constexpr float kOctaves = 48.f;               // the bins' range: weights down to 2^-48
+constexpr float kPhase = 2048.f;               // steps of a token's place in its bin: a million fit 32 bits
 constexpr double kScale = 4398046511104.0;     // 2^42: a million weights stay below 2^62
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;   // key of -inf
+constexpr unsigned kFull = 0xffffffffu;
 
-// Monotone key: larger float, larger key.  NaN counts as -inf, -0 as +0.
+using u64 = unsigned long long;
+
+// Monotone key: larger float, larger key.  -0 counts as +0 (NaN is made -inf on loading).
 __device__ __forceinline__ uint32_t key_of(float x) {
-  if (x != x) x = -CUDART_INF_F;
   const uint32_t b = __float_as_uint(x + 0.f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
+// A listed token: larger logit first, lower index first.
+__device__ __forceinline__ u64 entry_of(uint32_t key, int i) {
+  return (u64)key << 32 | (0xFFFFFFFFu - (uint32_t)i);
+}
+__device__ __forceinline__ uint32_t entry_key(u64 e) { return (uint32_t)(e >> 32); }
+__device__ __forceinline__ int entry_index(u64 e) { return (int)(0xFFFFFFFFu - (uint32_t)e); }
 
 struct SampleSmem {
-  unsigned long long hist[256];
-  unsigned long long part[kWarps];
-  double above[kWarps];
-  int ties[kWarps];
+  double table[16];                            // 2^(j/16)
+  union {
+    struct { unsigned count[kBins], phase[kBins]; } bin;
+    u64 hist[256];
+    struct { double w[kList], w_by_index[kList]; } list_w;
+  };
+  u64 list[kList], sorted[kList];
+  double part[kWarps], part2[kWarps];
+  int ipart[kWarps];
+  u64 upart[kWarps];
+  int n, pick, ties_left, around[2];
   uint32_t digit;
-  unsigned long long before;
-  int seg, seg_ties;
-  double target, seg_before, total;
+  u64 before;
+  double base, target, total;
 };
 
+// exp((x - m) / t) in 64 bits, as 2^(i/16 + r): a table of 2^(j/16), whose 16 entries lie in
+// banks of their own, and five terms of the exponential series in r (|r ln 2| < 0.022: 1.4e-13
+// relative).  Adding 1.5 * 2^48 rounds to sixteenths and leaves i in the low word.  What weighs
+// less than 2^-1000 weighs nothing.
 struct Weigher {
   float max;
-  double t;
-  __device__ __forceinline__ double operator()(uint32_t key) const {
-    const float x = value_of(key);
-    return x == max ? 1.0 : exp(((double)x - (double)max) / t);
+  double m, c;                                 // c = log2(e) / t
+  const double *table;
+  __device__ __forceinline__ double operator()(float x) const {
+    if (max == CUDART_INF_F) return x == max ? 1.0 : 0.0;
+    constexpr double kMagic = 422212465065984.0;
+    const double d = (double)x - m, s = fma(d, c, kMagic), r = fma(d, c, kMagic - s);
+    const int i = __double2loint(s), above = __double2hiint(s) - 0x42F80000;
+    double p = fma(r, 1.3333558146428443e-3, 9.6181291076284772e-3);
+    p = fma(p, r, 5.5504108664821580e-2);
+    p = fma(p, r, 2.4022650695910072e-1);
+    p = fma(p, r, 6.9314718055994531e-1);
+    const double y = table[i & 15], w = fma(y, p * r, y);
+    const bool in = above == i >> 31 && i >= -16000;          // -1000 <= z <= 0 (-inf is not)
+    return in ? __hiloint2double(__double2hiint(w) + ((i >> 4) << 20), __double2loint(w)) : 0.0;
   }
 };
 
-__device__ __forceinline__ unsigned long long fixed(double w) {
-  return (unsigned long long)__double2ll_rn(w * kScale);
+// A row of logits by aligned 16-byte vectors; the first and the last may be partial.
+template <typename T> struct Row {
+  static constexpr int N = 16 / sizeof(T);
+  const T *x;
+  int V, off;                                  // off: elements of vector 0 before the row
+  int vectors, full0, full1;                   // all, and the range that is whole
+  __device__ __forceinline__ Row(const T *p, int n) : x(p), V(n) {
+    off = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    vectors = (off + V + N - 1) / N;
+    full0 = off ? 1 : 0;
+    full1 = max(full0, (off + V) / N);
+  }
+  static __device__ __forceinline__ void widen(uint4 r, float (&v)[N]);
+  __device__ __forceinline__ uint4 raw(int vi) const {
+    return *reinterpret_cast<const uint4 *>(x - off + (long long)vi * N);
+  }
+  __device__ __forceinline__ int index(int vi, int j) const { return vi * N + j - off; }
+  // Vector vi, -inf in the places outside the row and for NaN.
+  __device__ __forceinline__ void load(int vi, float (&v)[N]) const {
+    if (vi >= full0 && vi < full1) {
+      widen(raw(vi), v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = fmaxf(v[j], -CUDART_INF_F);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int i = index(vi, j);
+        v[j] = i >= 0 && i < V ? fmaxf(to_f32(x[i]), -CUDART_INF_F) : -CUDART_INF_F;
+      }
+    }
+  }
+};
+template <> __device__ __forceinline__ void Row<float>::widen(uint4 r, float (&v)[4]) {
+  v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y);
+  v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+}
+template <> __device__ __forceinline__ void Row<__nv_bfloat16>::widen(uint4 r, float (&v)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+// Sums over the block in a fixed order; every thread gets the result.
+__device__ __forceinline__ double block_sum(double v, double *part) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = part[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) v += part[w];
+  return v;
+}
+
+// Exclusive prefix over the block's threads of a sum and a count.
+__device__ __forceinline__ void block_scan(double v, int c, SampleSmem &sm, double &v_before,
+                                           int &c_before, double &v_all, int &c_all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double s = v;
+  int k = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(kFull, s, o);
+    const int z = __shfl_up_sync(kFull, k, o);
+    if (lane >= o) {
+      s += y;
+      k += z;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    sm.part[warp] = s;
+    sm.ipart[warp] = k;
+  }
+  __syncthreads();
+  double b = 0.0;
+  int kb = 0;
+  v_all = 0.0;
+  c_all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) {
+      b = v_all;
+      kb = c_all;
+    }
+    v_all += sm.part[w];
+    c_all += sm.ipart[w];
+  }
+  const double up = __shfl_up_sync(kFull, s, 1);
+  v_before = b + (lane ? up : 0.0);
+  c_before = kb + k - c;
+}
+
+// sorted = list[0..n) in falling order, by counting what is larger (the entries differ).
+__device__ __forceinline__ void sort_list(const u64 *list, u64 *sorted, int n) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const u64 e = list[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += list[j] > e;
+    sorted[rank] = e;
+  }
+}
+
+__device__ __forceinline__ void put_token(const SampleArgs &a, int row, int token, double p) {
+  a.token[row] = token;
+  if (a.logprob) a.logprob[row] = (float)log(p);
+}
+
+// The token among the first n listed ones (sm.sorted, all kept, weights in sm.list_w.w): by index
+// order.  Called by the whole block.
+__device__ void pick_from_list(const SampleArgs &a, int row, SampleSmem &sm, int n, double u) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint32_t idx = (uint32_t)sm.sorted[i];           // falls as the index rises
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += (uint32_t)sm.sorted[j] > idx;
+    sm.list[rank] = sm.sorted[i];
+    sm.list_w.w_by_index[rank] = sm.list_w.w[i];
+  }
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x, per = (n + 31) / 32, lo = min(n, lane * per), hi = min(n, lo + per);
+  double own = 0.0;
+  for (int i = lo; i < hi; ++i) own += sm.list_w.w_by_index[i];
+  double s = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(kFull, s, o);
+    if (lane >= o) s += y;
+  }
+  const double total = __shfl_sync(kFull, s, 31), target = u * total;
+  const unsigned live = __ballot_sync(kFull, own > 0.0);
+  const unsigned hit = __ballot_sync(kFull, own > 0.0 && s > target);
+  const int src = hit ? __ffs(hit) - 1 : 31 - __clz(live);
+  double c = __shfl_up_sync(kFull, s, 1);
+  if (lane == 0) c = 0.0;
+  if (lane == src) {
+    int at = lo;
+    for (int i = lo; i < hi; ++i) {
+      const double w = sm.list_w.w_by_index[i];
+      if (w > 0.0) at = i;
+      c += w;
+      if (w > 0.0 && c > target) break;
+    }
+    put_token(a, row, entry_index(sm.list[at]), sm.list_w.w_by_index[at] / total);
+  }
+}
+
+// Sorts the listed tokens and weighs them (sm.sorted, sm.list_w.w); returns how many of them start
+// below top_p of the mass, `above` of which lies before the list and `below` behind it, or 0 if
+// the border is not inside it.  Called by the whole block.
+__device__ int border_in_list(const Weigher &weight, SampleSmem &sm, int n, double above, double below,
+                              double top_p) {
+  sort_list(sm.list, sm.sorted, n);
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    sm.list_w.w[i] = weight(value_of(entry_key(sm.sorted[i])));
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, per = (n + 31) / 32, lo = min(n, lane * per), hi = min(n, lo + per);
+    double s = 0.0;
+    for (int i = lo; i < hi; ++i) s += sm.list_w.w[i];
+    const double mine = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(kFull, s, o);
+      if (lane >= o) s += y;
+    }
+    const double end = above + __shfl_sync(kFull, s, 31), goal = top_p * (end + below);
+    double at = above + (s - mine);
+    int kept = 0;
+    for (int i = lo; i < hi; ++i) {
+      kept += at < goal;
+      at += sm.list_w.w[i];
+    }
+    kept = __reduce_add_sync(kFull, kept);
+    // inside: the first listed token is kept, and the list ends at or past the goal
+    if (lane == 0) sm.pick = kept > 0 && (kept < n || end >= goal) ? kept : 0;
+  }
+  __syncthreads();
+  return sm.pick;
+}
+
+// The nearest bins with tokens on either side of sm.pick (itself where there is none; the last
+// bin, of the weights below the range, does not count).  Called by the whole block.
+__device__ void filled_around(SampleSmem &sm, int &before, int &after) {
+  __syncthreads();
+  const int pick = sm.pick;
+  int lo = -1, hi = kBins;
+#pragma unroll
+  for (int j = 0; j < kBins / kThreads; ++j) {
+    const int b = threadIdx.x * (kBins / kThreads) + j;
+    if (sm.bin.count[b] && b < kBins - 1) {
+      if (b < pick) lo = max(lo, b);
+      if (b > pick) hi = min(hi, b);
+    }
+  }
+  lo = __reduce_max_sync(kFull, lo);
+  hi = __reduce_min_sync(kFull, hi);
+  if (threadIdx.x == 0) {
+    sm.around[0] = -1;
+    sm.around[1] = kBins;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    atomicMax(&sm.around[0], lo);
+    atomicMin(&sm.around[1], hi);
+  }
+  __syncthreads();
+  before = sm.around[0] < 0 ? pick : sm.around[0];
+  after = sm.around[1] == kBins ? pick : sm.around[1];
+}
+
+// Border of top-k (by count) or of top-p (by mass) through the bits of the keys, eight at a
+// time: masses are 64-bit integers (weight * 2^42), whose order in the atomics does not matter.
+// General and slow: up to five reads of the row.
+template <typename T>
+__device__ void descend(const Row<T> &row, const Weigher &weight, SampleSmem &sm, bool by_mass,
+                        int top_k, float top_p, uint32_t &edge, int &n_edge) {
+  const int tid = threadIdx.x;
+  const auto fixed = [](double w) { return (u64)__double2ll_rn(w * kScale); };
+  double goal = 0.0;
+  if (by_mass) {
+    u64 mass = 0;
+    for (int i = tid; i < row.V; i += kThreads) {
+      const float x = fmaxf(to_f32(row.x[i]), -CUDART_INF_F);
+      if (key_of(x) > edge) mass += fixed(weight(x));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(kFull, mass, o);
+    __syncthreads();
+    if ((tid & 31) == 0) sm.upart[tid >> 5] = mass;
+    __syncthreads();
+    mass = edge ? n_edge * fixed(weight(value_of(edge))) : 0;
+    for (int w = 0; w < kWarps; ++w) mass += sm.upart[w];
+    goal = (double)top_p * (double)mass;
+  }
+  uint32_t prefix = 0, mask = 0;
+  u64 before = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    __syncthreads();
+    if (tid < 256) sm.hist[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < row.V; i += kThreads) {
+      const float x = fmaxf(to_f32(row.x[i]), -CUDART_INF_F);
+      const uint32_t key = key_of(x);
+      if (key >= edge && (key & mask) == prefix)
+        atomicAdd(&sm.hist[key >> shift & 255], by_mass ? fixed(weight(x)) : 1ull);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      u64 c = before, at = before;
+      int pick = -1;
+      for (int d = 255; d >= 0; --d) {
+        if (!sm.hist[d]) continue;
+        // the last digit that starts below the goal (the first one always does or is taken)
+        if (pick >= 0 && !(by_mass ? (double)c < goal : c < (u64)top_k)) break;
+        pick = d;
+        at = c;
+        c += sm.hist[d];
+      }
+      sm.digit = pick;
+      sm.before = at;
+    }
+    __syncthreads();
+    before = sm.before;
+    prefix |= sm.digit << shift;
+    mask |= 255u << shift;
+  }
+  if (!by_mass) {
+    edge = prefix;
+    n_edge = top_k - (int)before;
+    return;
+  }
+  // equals at the border: kept while the mass before them is below the goal
+  const u64 w = fixed(weight(value_of(prefix)));
+  const int most = prefix == edge ? n_edge : row.V;
+  int n = 1;
+  if (w) {
+    const double d = (goal - (double)before) / (double)w;
+    n = d >= (double)most ? most : max(1, (int)ceil(d));
+  }
+  edge = prefix;
+  n_edge = min(n, most);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
+  constexpr int N = Row<T>::N;
   __shared__ SampleSmem sm;
-  const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, V = a.V;
-  const T *x = static_cast<const T *>(a.logits) + (long long)row * a.stride;
-  const float u = a.uniform[row], t = a.temperature ? a.temperature[row] : 1.f;
-  const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
-  const int top_k = a.top_k ? a.top_k[row] : 0;
+  const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Row<T> row(static_cast<const T *>(a.logits) + (long long)r * a.stride, a.V);
+  const float u = a.uniform[r], t = a.temperature ? a.temperature[r] : 1.f;
+  const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f;
+  const int k_asked = a.top_k ? a.top_k[r] : 0, top_k = k_asked > 0 && k_asked < a.V ? k_asked : 0;
   if (!(u >= 0.f && u <= 1.f && t >= 0.f && t < CUDART_INF_F && top_p >= 0.f && top_p <= 1.f &&
         min_p >= 0.f && min_p <= 1.f)) {
-    if (tid == 0) set_status(a.ws, TV_ERR_BAD_PARAM, row);
+    if (tid == 0) set_status(a.ws, TV_ERR_BAD_PARAM, r);
     return;
   }
 
-  // ---- largest logit, lowest index of it -------------------------------------------------
-  unsigned long long best = 0;
-  for (int i = tid; i < V; i += kThreads) {
-    const unsigned long long c = (unsigned long long)key_of(to_f32(x[i])) << 32 | (0xFFFFFFFFu - i);
-    best = c > best ? c : best;
-  }
+  // ---- first read: the largest logit of each thread's stripe, and of the row ---------------
+  float own = -CUDART_INF_F;
+#pragma unroll 4
+  for (int vi = row.full0 + tid; vi < row.full1; vi += kThreads) {
+    float v[N];
+    Row<T>::widen(row.raw(vi), v);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const unsigned long long c = __shfl_xor_sync(0xffffffffu, best, o);
-    best = c > best ? c : best;
+    for (int j = 0; j < N; ++j) own = fmaxf(own, v[j]);      // a NaN loses
   }
-  if (lane == 0) sm.part[warp] = best;
+  // the partial vectors belong to the last two threads' stripes
+  const int ragged = tid == kThreads - 1 && row.full0 > 0 ? 0
+                     : tid == kThreads - 2 && row.full1 < row.vectors ? row.full1 : -1;
+  if (ragged >= 0) {
+    float v[N];
+    row.load(ragged, v);
+#pragma unroll
+    for (int j = 0; j < N; ++j) own = fmaxf(own, v[j]);
+  }
+  const uint32_t own_key = key_of(own);
+  uint32_t max_key = __reduce_max_sync(kFull, own_key);
+  if (lane == 0) sm.ipart[warp] = (int)max_key;
+  if (tid < 16) sm.table[tid] = exp2((double)tid / 16.0);
+  if (tid == 0) sm.n = 0;
   __syncthreads();
-  best = sm.part[0];
-  for (int w = 1; w < kWarps; ++w) best = sm.part[w] > best ? sm.part[w] : best;
-  const uint32_t max_key = best >> 32;
-  if (max_key == kKeyNegInf || t == 0.f) {
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) max_key = max(max_key, (uint32_t)sm.ipart[w]);
+  if (max_key == kKeyNegInf) {
     if (tid == 0) {
-      const bool none = max_key == kKeyNegInf;
-      a.token[row] = none ? -1 : (int)(0xFFFFFFFFu - (uint32_t)best);
-      if (a.logprob) a.logprob[row] = none ? -CUDART_INF_F : 0.f;
+      a.token[r] = -1;
+      if (a.logprob) a.logprob[r] = -CUDART_INF_F;
     }
     return;
   }
-  const Weigher weight{value_of(max_key), (double)t};
-
-  // ---- kept: keys above `edge`, and the first `n_edge` equal to it ------------------------
-  uint32_t edge = 0;
-  int n_edge = V;
-  if (top_k > 0 && top_k < V) {
-    uint32_t prefix = 0, mask = 0;
-    unsigned long long before = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) sm.hist[tid] = 0;
-      __syncthreads();
-      for (int i = tid; i < V; i += kThreads) {
-        const uint32_t key = key_of(to_f32(x[i]));
-        if ((key & mask) == prefix) atomicAdd(&sm.hist[key >> shift & 255], 1ull);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int d = 255;
-        unsigned long long c = before;
-        for (; d > 0 && c + sm.hist[d] < (unsigned long long)top_k; --d) c += sm.hist[d];
-        sm.digit = d;
-        sm.before = c;
-      }
-      __syncthreads();
-      before = sm.before;
-      prefix |= sm.digit << shift;
-      mask |= 255u << shift;
-      __syncthreads();
-    }
-    edge = prefix;
-    n_edge = top_k - (int)before;
-  }
-  if (top_p < 1.f) {
-    // mass of the survivors of top-k
-    unsigned long long mass = 0;
-    for (int i = tid; i < V; i += kThreads) {
-      const uint32_t key = key_of(to_f32(x[i]));
-      if (key > edge) mass += fixed(weight(key));
-    }
+  const float top = value_of(max_key);
+  // visits the stripe of this thread again: f(value, index)
+  const auto stripe = [&](auto f) {
+#pragma unroll 4
+    for (int vi = row.full0 + tid; vi < row.full1; vi += kThreads) {
+      float v[N];
+      Row<T>::widen(row.raw(vi), v);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    if (lane == 0) sm.part[warp] = mass;
+      for (int j = 0; j < N; ++j) f(fmaxf(v[j], -CUDART_INF_F), row.index(vi, j));
+    }
+    if (ragged >= 0) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int i = row.index(ragged, j);
+        if (i >= 0 && i < row.V) f(fmaxf(to_f32(row.x[i]), -CUDART_INF_F), i);
+      }
+    }
+  };
+
+  // ---- temperature zero, or one token kept: the lowest index of the largest logit ---------
+  if (t == 0.f || top_k == 1 || top_p == 0.f) {
+    unsigned first = 0xFFFFFFFFu;
+    if (own_key == max_key)
+      stripe([&](float x, int i) { if (x == top) first = min(first, (unsigned)i); });
+    first = __reduce_min_sync(kFull, first);
     __syncthreads();
-    mass = edge ? n_edge * fixed(weight(edge)) : 0;
-    for (int w = 0; w < kWarps; ++w) mass += sm.part[w];
-    const double goal = (double)top_p * (double)mass;
-    uint32_t prefix = 0, mask = 0;
-    unsigned long long before = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      __syncthreads();
-      if (tid < 256) sm.hist[tid] = 0;
-      __syncthreads();
-      for (int i = tid; i < V; i += kThreads) {
-        const uint32_t key = key_of(to_f32(x[i]));
-        if (key >= edge && (key & mask) == prefix)
-          atomicAdd(&sm.hist[key >> shift & 255], fixed(weight(key)));
-      }
-      __syncthreads();
-      if (tid == 0) {
-        // the last digit that holds mass and starts below the goal (the largest logit holds
-        // the most, so there is one)
-        unsigned long long c = before;
-        int pick = -1;
-        unsigned long long at = before;
-        for (int d = 255; d >= 0; --d) {
-          if (!sm.hist[d]) continue;
-          if (pick >= 0 && !((double)c < goal)) break;
-          pick = d;
-          at = c;
-          c += sm.hist[d];
-        }
-        sm.digit = pick;
-        sm.before = at;
-      }
-      __syncthreads();
-      before = sm.before;
-      prefix |= sm.digit << shift;
-      mask |= 255u << shift;
+    if (lane == 0) sm.ipart[warp] = (int)first;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 0; w < kWarps; ++w) first = min(first, (unsigned)sm.ipart[w]);
+      a.token[r] = (int)first;
+      if (a.logprob) a.logprob[r] = 0.f;
     }
-    // equals at the border: kept while the mass before them is below the goal
-    const unsigned long long w = fixed(weight(prefix));
-    int most = prefix == edge ? n_edge : V, n = 1;
-    if (w) {
-      const double d = (goal - (double)before) / (double)w;
-      n = d >= (double)most ? most : max(1, (int)ceil(d));
-    }
-    edge = prefix;
-    n_edge = min(n, most);
+    return;
   }
 
-  // ---- kept weight by segments of the vocabulary, one warp each --------------------------
-  const int seg = ((V + kWarps - 1) / kWarps + 31) / 32 * 32;
-  const int s0 = min(V, warp * seg), s1 = min(V, s0 + seg);
-  double above = 0.0;
-  int ties = 0;
-  for (int i = s0 + lane; i < s1; i += 32) {
-    const uint32_t key = key_of(to_f32(x[i]));
-    if (key > edge) {
-      const double w = weight(key);
-      if (w >= (double)min_p) above += w;
-    } else if (key == edge) {
-      ++ties;
+  const Weigher weight{top, (double)top, 1.4426950408889634 / (double)t, sm.table};
+  uint32_t edge = 0;                  // kept: keys above `edge`, and the first n_edge equal to it
+  int n_edge = a.V;
+  bool by_edge = false;               // the border is known from a descent
+
+  // ---- small top-k: a short list ------------------------------------------------------------
+  if (top_k && top_k <= kSmallK) {
+    // a bound that at least top_k logits reach: the top_k-th largest stripe maximum, to 20 bits
+    uint32_t bound = 0;
+    for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1)
+      if (__syncthreads_count(own_key >= (bound | bit)) >= top_k) bound |= bit;
+    // exp(-760) is zero in 64 bits: logits below that (masked ones) are not worth a place
+    const float bound_x = fmaxf(value_of(max(bound, kKeyNegInf)), top - 760.f * t);
+    if (own_key >= bound)
+      stripe([&](float x, int i) {
+        if (x >= bound_x && x > -CUDART_INF_F) {
+          const int at = atomicAdd(&sm.n, 1);
+          if (at < kList) sm.list[at] = entry_of(key_of(x), i);
+        }
+      });
+    __syncthreads();
+    const int n = sm.n, k = min(top_k, n);
+    if (n <= kList) {
+      sort_list(sm.list, sm.sorted, n);
+      __syncthreads();
+      for (int i = tid; i < k; i += kThreads)
+        sm.list_w.w[i] = weight(value_of(entry_key(sm.sorted[i])));
+      __syncthreads();
+      if (warp == 0) {
+        // the prefixes of top-p and min-p: lanes take runs of the sorted list
+        const int per = (k + 31) / 32, lo = min(k, lane * per), hi = min(k, lo + per);
+        double s = 0.0;
+        for (int i = lo; i < hi; ++i) s += sm.list_w.w[i];
+        const double mine = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y = __shfl_up_sync(kFull, s, o);
+          if (lane >= o) s += y;
+        }
+        const double goal = (double)top_p * __shfl_sync(kFull, s, 31);
+        double c = s - mine;
+        int kept = 0;
+        for (int i = lo; i < hi; ++i) {
+          const double w = sm.list_w.w[i];
+          kept += (i == 0 || top_p >= 1.f || c < goal) && w >= (double)min_p;
+          c += w;
+        }
+        kept = __reduce_add_sync(kFull, kept);
+        if (lane == 0) sm.pick = kept;
+      }
+      __syncthreads();
+      pick_from_list(a, r, sm, sm.pick, (double)u);
+      return;
+    }
+    __syncthreads();
+  }
+  if (top_k) {
+    descend(row, weight, sm, false, top_k, top_p, edge, n_edge);
+    by_edge = true;
+  }
+
+  // ---- top-p: the border ---------------------------------------------------------------------
+  const int seg = (row.vectors + kWarps - 1) / kWarps;        // vectors per warp's segment
+  const int s0 = min(row.vectors, warp * seg), s1 = min(row.vectors, s0 + seg);
+  double kept_here = 0.0;             // kept weight above the border in this warp's segment
+  int ties = 0;                       // equals of the border in it
+  bool have_sums = false;
+  if (top_p < 1.f && !by_edge) {
+    int listed = 0;                   // tokens of the list before the border
+    const float scale = (float)(weight.c * (double)(kBins / kOctaves));
+    const auto bin_of = [&](float x, float &z) {
+      z = (top - x) * scale;
+      if (x == top) z = 0.f;
+      return min((int)z, kBins - 1);                          // monotone in x; saturates
+    };
+    for (int i = tid; i < kBins; i += kThreads) sm.bin.count[i] = sm.bin.phase[i] = 0;
+    __syncthreads();
+    unsigned bits = 0;                // that any logit has
+    stripe([&](float x, int) {
+      float z;
+      bits |= __float_as_uint(x);
+      const int b = bin_of(x, z);
+      if (b < kBins - 1) {
+        atomicAdd(&sm.bin.count[b], 1u);
+        atomicAdd(&sm.bin.phase[b], (unsigned)((z - (float)b) * kPhase));
+      }
+    });
+    __syncthreads();
+    // approximate masses: a bin's tokens at their mean place in it (1e-5: the bin is 1.6% wide)
+    constexpr int kPer = kBins / kThreads;
+    double mass[kPer], mine = 0.0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int b = tid * kPer + j;
+      const float count = (float)sm.bin.count[b];
+      const float place = ((float)sm.bin.phase[b] / fmaxf(count, 1.f) + 0.5f) / kPhase;
+      mass[j] = (double)count * exp2f(-((float)b + place) * (kOctaves / kBins));
+      mine += mass[j];
+    }
+    double c, all;
+    int unused, unused_all;
+    block_scan(mine, 0, sm, c, unused, all, unused_all);
+    double goal = (double)top_p * all;          // near enough to name the bin
+    if (tid == 0) {
+      sm.pick = 0;
+      sm.digit = 0;
+    }
+    __syncthreads();
+    int last = 0;                     // the last bin with tokens that starts below the goal
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (sm.bin.count[tid * kPer + j] && c < goal) last = tid * kPer + j;
+      c += mass[j];
+    }
+    last = __reduce_max_sync(kFull, last);
+    if (lane == 0) atomicMax(&sm.pick, last);
+    // the border is in that bin, or next to its ends: from the bin with tokens before it to the
+    // one after it
+    int b0, b1;
+    filled_around(sm, b0, b1);
+    int n_range = sm.bin.count[sm.pick];
+    n_range += b0 < sm.pick ? sm.bin.count[b0] : 0;
+    n_range += b1 > sm.pick ? sm.bin.count[b1] : 0;
+    bool found = false;
+    if (sm.pick < kBins - 2 && n_range <= kList) {
+      double above = 0.0, below = 0.0;
+      for (int vi = s0 + lane; vi < s1; vi += 32) {
+        float v[N];
+        row.load(vi, v);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          float z;
+          const int b = bin_of(v[j], z);
+          const double w = weight(v[j]);
+          if (b < b0) {
+            above += w;
+            if (w >= (double)min_p) kept_here += w;
+          } else if (b > b1) {
+            below += w;
+          } else {
+            sm.list[atomicAdd(&sm.n, 1)] = entry_of(key_of(v[j]), row.index(vi, j));
+          }
+        }
+      }
+      above = block_sum(above, sm.part);
+      below = block_sum(below, sm.part);
+      listed = border_in_list(weight, sm, sm.n, above, below, (double)top_p);
+      found = listed > 0;
+    } else if (sm.pick < kBins - 2) {
+      // count the range by parts of its keys; `grain` low bits tell no two of the row's logits
+      // apart, and a part is 2^shift of what is left of a key
+      bits = __reduce_or_sync(kFull, bits);
+      if (lane == 0) atomicOr(&sm.digit, bits);
+      __syncthreads();
+      const int grain = min(20, __ffs(sm.digit | 1u << 20) - 1);
+      const uint32_t hi = (b0 ? key_of(__double2float_ru((double)top - (b0 - 0.05) / (double)scale)) : max_key) >> grain;
+      const uint32_t lo = key_of(__double2float_rd((double)top - (b1 + 1.05) / (double)scale)) >> grain;
+      int shift = 0;
+      while ((hi - lo) >> shift >= kBins) ++shift;
+      const auto part_of = [&](uint32_t key) { return (int)min((hi - (key >> grain)) >> shift, (uint32_t)kBins - 1); };
+      for (int i = tid; i < kBins; i += kThreads) sm.bin.count[i] = 0;
+      __syncthreads();
+      double above = 0.0, below = 0.0;
+      for (int vi = s0 + lane; vi < s1; vi += 32) {
+        float v[N];
+        row.load(vi, v);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          float z;
+          const int b = bin_of(v[j], z);
+          if (b >= b0 && b <= b1) {
+            atomicAdd(&sm.bin.count[part_of(key_of(v[j]))], 1u);
+            continue;
+          }
+          const double w = weight(v[j]);
+          if (b < b0) {
+            above += w;
+            if (w >= (double)min_p) kept_here += w;
+          } else {
+            below += w;
+          }
+        }
+      }
+      above = block_sum(above, sm.part);
+      below = block_sum(below, sm.part);
+      // the key in the middle of a part (its only one where shift is 0)
+      const auto key_in = [&](int p) {
+        const uint32_t k = (hi - ((uint32_t)p << shift) - ((1u << shift) >> 1)) << grain;
+        return k & 0x80000000u ? k : k | ((1u << grain) - 1);
+      };
+      mine = 0.0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int p = tid * kPer + j, count = sm.bin.count[p];
+        mass[j] = count ? count * weight(value_of(key_in(p))) : 0.0;
+        mine += mass[j];
+      }
+      block_scan(mine, 0, sm, c, unused, all, unused_all);
+      c += above;
+      all += above;                             // what lies before and in the range
+      goal = (double)top_p * (all + below);
+      if (tid == 0) sm.pick = -1;
+      __syncthreads();
+      last = -1;
+      double start = 0.0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (sm.bin.count[tid * kPer + j] && c < goal) {
+          last = tid * kPer + j;
+          start = c;
+        }
+        c += mass[j];
+      }
+      const int warp_last = __reduce_max_sync(kFull, last);
+      if (lane == 0) atomicMax(&sm.pick, warp_last);
+      __syncthreads();
+      const int part = sm.pick;
+      int p0 = part, p1 = part;
+      if (part >= 0) filled_around(sm, p0, p1);
+      if (part >= 0 && all >= goal && shift == 0) {
+        // equals at the border: kept while the mass before them is below the goal
+        if (part == last) {
+          const int count = sm.bin.count[part];
+          const double d = (goal - start) / weight(value_of(key_in(part)));
+          sm.ties_left = d >= (double)count ? count : max(1, (int)ceil(d));
+        }
+        __syncthreads();
+        edge = key_in(part);
+        n_edge = sm.ties_left;
+        found = true;
+        for (int vi = s0 + lane; vi < s1; vi += 32) {
+          float v[N];
+          row.load(vi, v);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const uint32_t key = key_of(v[j]);
+            ties += key == edge;
+            float z;
+            if (key > edge && bin_of(v[j], z) >= b0) {
+              const double w = weight(v[j]);
+              if (w >= (double)min_p) kept_here += w;
+            }
+          }
+        }
+      } else if (part >= 0 && all >= goal) {
+        double between = 0.0, after = 0.0;
+        for (int vi = s0 + lane; vi < s1; vi += 32) {
+          float v[N];
+          row.load(vi, v);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            float z;
+            const int b = bin_of(v[j], z);
+            if (b < b0 || b > b1) continue;
+            const uint32_t key = key_of(v[j]);
+            const int p = part_of(key);
+            if (p < p0) {
+              const double w = weight(v[j]);
+              between += w;
+              if (w >= (double)min_p) kept_here += w;
+            } else if (p > p1) {
+              after += weight(v[j]);
+            } else {
+              const int at = atomicAdd(&sm.n, 1);
+              if (at < kList) sm.list[at] = entry_of(key, row.index(vi, j));
+            }
+          }
+        }
+        between = block_sum(between, sm.part);
+        after = block_sum(after, sm.part);
+        if (sm.n <= kList)
+          listed = border_in_list(weight, sm, sm.n, above + between, after + below, (double)top_p);
+        found = listed > 0;
+      }
+    }
+    have_sums = found;
+    if (listed > 0) {
+      // the border, its kept equals, and the segment's share of the list
+      edge = entry_key(sm.sorted[listed - 1]);
+      const int n = sm.n;
+      int equal = 0;
+      for (int i = lane; i < n; i += 32) {
+        const int vi = (entry_index(sm.sorted[i]) + row.off) / N;
+        const uint32_t key = entry_key(sm.sorted[i]);
+        const bool here = vi >= s0 && vi < s1;
+        equal += key == edge && i < listed;
+        ties += key == edge && here;
+        if (here && key > edge && sm.list_w.w[i] >= (double)min_p) kept_here += sm.list_w.w[i];
+      }
+      n_edge = __reduce_add_sync(kFull, equal);
+    }
+    if (!found) {
+      __syncthreads();
+      descend(row, weight, sm, true, top_k, top_p, edge, n_edge);
+    }
+  } else if (top_p < 1.f) {
+    descend(row, weight, sm, true, top_k, top_p, edge, n_edge);
+  }
+
+  // ---- kept weight above the border, and equals of it, by segments of the vocabulary --------
+  const double w_raw = edge ? weight(value_of(edge)) : 0.0;
+  const double w_edge = w_raw >= (double)min_p ? w_raw : 0.0;
+  // a logit below this is out by min_p without its weight (the bound's own rounding aside)
+  float low_x = -CUDART_INF_F;
+  if (min_p > 0.f && top < CUDART_INF_F) {
+    const float low = (float)((double)top + (double)t * (log((double)min_p) - 1e-3));
+    low_x = low - fabsf(low) * 1e-6f;
+  }
+  if (!have_sums) {
+    kept_here = 0.0;
+    ties = 0;
+    for (int vi = s0 + lane; vi < s1; vi += 32) {
+      float v[N];
+      row.load(vi, v);
+      if (!edge && min_p == 0.f) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) kept_here += weight(v[j]);
+        continue;
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t key = key_of(v[j]);
+        if (key > edge) {
+          if (v[j] >= low_x) {
+            const double w = weight(v[j]);
+            if (w >= (double)min_p) kept_here += w;
+          }
+        } else if (key == edge) {
+          ++ties;
+        }
+      }
     }
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    above += __shfl_xor_sync(0xffffffffu, above, o);
-    ties += __shfl_xor_sync(0xffffffffu, ties, o);
-  }
+  for (int o = 16; o; o >>= 1) kept_here += __shfl_xor_sync(kFull, kept_here, o);
+  ties = __reduce_add_sync(kFull, ties);
+  __syncthreads();
   if (lane == 0) {
-    sm.above[warp] = above;
-    sm.ties[warp] = ties;
+    sm.part[warp] = kept_here;
+    sm.ipart[warp] = ties;
   }
-  const double w_raw = weight(edge), w_edge = w_raw >= (double)min_p ? w_raw : 0.0;
   __syncthreads();
   if (tid == 0) {
     double total = 0.0;
     int left = n_edge;
     for (int w = 0; w < kWarps; ++w) {
-      const int k = min(left, sm.ties[w]);
-      total += sm.above[w] + k * w_edge;
+      const int k = min(left, sm.ipart[w]);
+      total += sm.part[w] + k * w_edge;
       left -= k;
     }
     const double target = (double)u * total;
     double c = 0.0;
     left = n_edge;
-    sm.seg = -1;
     for (int w = 0; w < kWarps; ++w) {
-      const int k = min(left, sm.ties[w]);
-      const double m = sm.above[w] + k * w_edge;
-      if (m > 0.0) {
-        sm.seg = w;
-        sm.seg_ties = left;
-        sm.seg_before = c;
+      const int k = min(left, sm.ipart[w]);
+      const double m = sm.part[w] + k * w_edge;
+      if (m > 0.0) {                  // the last segment with weight, or the first past the target
+        sm.pick = w;
+        sm.ties_left = left;
+        sm.base = c;
         if (c + m > target) break;
       }
       c += m;
@@ -239,43 +844,77 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a) {
     sm.target = target;
   }
   __syncthreads();
-  if (warp != sm.seg) return;
 
-  // ---- the token, by the warp that owns its segment ----------------------------------------
-  double c = sm.seg_before;
-  int left = sm.seg_ties, token = -1;
-  double w_token = 0.0;
-  for (int i0 = s0; i0 < s1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < s1 ? key_of(to_f32(x[i])) : 0;
-    const bool tie = i < s1 && key == edge;
-    const unsigned tied = __ballot_sync(0xffffffffu, tie);
-    const int rank = __popc(tied & ((1u << lane) - 1));
-    double w = 0.0;
-    if (i < s1 && (key > edge || (tie && rank < left))) {
-      w = weight(key);
-      if (w < (double)min_p) w = 0.0;
-    }
-    left -= min(left, __popc(tied));
-    double sum = w;
+  // ---- the token: the whole block over its segment --------------------------------------------
+  const int e0 = min(row.vectors, sm.pick * seg), e1 = min(row.vectors, e0 + seg);
+  const double target = sm.target, total = sm.total;
+  double base = sm.base;
+  int left = sm.ties_left;
+  for (int v0 = e0; v0 < e1; v0 += kThreads) {
+    const int vi = v0 + tid;
+    float v[N];
+    double above = 0.0;
+    int eq = 0;
+    if (vi < e1) {
+      row.load(vi, v);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
+      for (int j = 0; j < N; ++j) {
+        const uint32_t key = key_of(v[j]);
+        if (key > edge) {
+          if (v[j] >= low_x) {
+            const double w = weight(v[j]);
+            if (w >= (double)min_p) above += w;
+          }
+        } else if (key == edge) {
+          ++eq;
+        }
+      }
     }
-    const unsigned live = __ballot_sync(0xffffffffu, w > 0.0);
-    const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && c + sum > sm.target);
-    if (live) {                          // the last kept token so far, in case none is past
-      const int src = hit ? __ffs(hit) - 1 : 31 - __clz(live);
-      token = i0 + src;
-      w_token = __shfl_sync(0xffffffffu, w, src);
+    double a_before, a_all;
+    int c_before, c_all;
+    block_scan(above, eq, sm, a_before, c_before, a_all, c_all);
+    const int mine = min(max(left - c_before, 0), eq);
+    const double before = base + a_before + min(c_before, left) * w_edge;
+    const double own_w = above + mine * w_edge;
+    const unsigned live = __ballot_sync(kFull, own_w > 0.0);
+    const unsigned hit = __ballot_sync(kFull, own_w > 0.0 && before + own_w > target);
+    // first thread past the target; without one, the last that holds kept weight
+    if (tid == 0) {
+      sm.n = kThreads;
+      sm.digit = 0;
     }
-    if (hit) break;
-    c += __shfl_sync(0xffffffffu, sum, 31);
-  }
-  if (lane == 0) {
-    a.token[row] = token;
-    if (a.logprob) a.logprob[row] = (float)log(w_token / sm.total);
+    __syncthreads();
+    if (lane == 0 && hit) atomicMin(&sm.n, warp * 32 + __ffs(hit) - 1);
+    if (lane == 0 && live) atomicMax(&sm.digit, (unsigned)(warp * 32 + 32 - __clz(live)));
+    __syncthreads();
+    const bool past = sm.n < kThreads;
+    const int src = past ? sm.n : (int)sm.digit - 1;
+    if (tid == src) {
+      double c = before, w_at = 0.0;
+      int at = -1, k = mine;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t key = key_of(v[j]);
+        double w = 0.0;
+        if (key > edge) {
+          w = weight(v[j]);
+          if (w < (double)min_p) w = 0.0;
+        } else if (key == edge && k > 0) {
+          --k;
+          w = w_edge;
+        }
+        if (w > 0.0 && !(at >= 0 && c > target)) {
+          at = row.index(vi, j);
+          w_at = w;
+          c += w;
+        }
+      }
+      put_token(a, r, at, w_at / total);
+    }
+    if (past) return;
+    base += a_all + min(c_all, left) * w_edge;
+    left -= min(c_all, left);
+    __syncthreads();
   }
 }
 
