@@ -79,9 +79,13 @@ tv_status tv_prefill(const tv_problem *p, const void *q, const void *k, const vo
   if (p->mode == TV_MODE_GDN ? !arr(b, none) : !opt(b)) return TV_ERR_INVALID_ARG;
   if (workspace_bytes < tv_prefill_workspace_size(p)) return TV_ERR_INVALID_ARG;
   if (!states_apart(p, S_in, S_out)) return TV_ERR_INVALID_ARG;
-  if (p->kernel == TV_KERNEL_TC) return TV_ERR_UNSUPPORTED;
+  const bool tc = p->in_dtype == TV_BF16 && p->dk == 128 && p->dv == 128;
+  if (p->kernel == TV_KERNEL_TC && !tc) return TV_ERR_UNSUPPORTED;
   if (p->B == 0) return TV_OK;
   const SequenceArgs a = sequence_args(p, q, k, v, log_a, b, seq_offsets, S_in, out, S_out, workspace);
+  if (tc && !none && p->kernel != TV_KERNEL_SIMT)
+    return record_cuda_error(
+        launch_prefill_tc(a, p->mode, p->out_dtype, reinterpret_cast<cudaStream_t>(stream)));
   return record_cuda_error(launch_prefill_simt(a, p->mode, p->in_dtype, p->out_dtype,
                                                reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -48,6 +48,7 @@ __device__ __forceinline__ bool sequence_range(const int32_t *offsets, int s, in
 
 cudaError_t launch_prefill_simt(const SequenceArgs &a, int mode, int in_dtype, int out_dtype,
                                 cudaStream_t st);
+cudaError_t launch_prefill_tc(const SequenceArgs &a, int mode, int out_dtype, cudaStream_t st);
 cudaError_t launch_decode_step(const SequenceArgs &a, int mode, int in_dtype, int out_dtype,
                                cudaStream_t st);
 cudaError_t launch_sample(const SampleArgs &a, int in_dtype, cudaStream_t st);
