@@ -4,9 +4,9 @@
 //
 // The rows of S are independent given k and q: eight lanes hold a row in registers for the
 // whole prompt (NK float4 each), and a CTA of 128 threads holds 16 rows of one (sequence,
-// head).  A token costs the chain S k -> u -> S' (one dot product, three shuffles, two
-// multiply-adds); o hangs off the chain.  Tokens arrive in double-buffered tiles of kTile
-// by cp.async in their own type and are widened as they are read.  fp32 throughout.
+// head).  A token costs the chain u -> S' -> S' k (the next token's dot product, in four running
+// sums, and three shuffles); o = S' q is formed beside it.  Tokens arrive in double-buffered
+// tiles of kTile by cp.async in their own type and are widened as they are read.  fp32 throughout.
 #include "serving.cuh"
 #include "tc_ptx.cuh"
 
@@ -31,9 +31,14 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
   return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u),
                      __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
+// Four running sums (a single one would make a chain of the whole row).
+__device__ __forceinline__ void dot4(float4 a, float4 b, float4 &s) {
+  s.x = fmaf(a.x, b.x, s.x);
+  s.y = fmaf(a.y, b.y, s.y);
+  s.z = fmaf(a.z, b.z, s.z);
+  s.w = fmaf(a.w, b.w, s.w);
 }
+__device__ __forceinline__ float sum4(float4 s) { return (s.x + s.y) + (s.z + s.w); }
 __device__ __forceinline__ float sum8(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   x += __shfl_xor_sync(0xffffffffu, x, 2);
@@ -105,36 +110,42 @@ __global__ void __launch_bounds__(kThreads) prefill_kernel(SequenceArgs a) {
     if (t0 + kTile < n)
       fetch<Tin, kGdn>(a, tile[buf ^ 1], (size_t)lo + t0 + kTile, min(kTile, n - t0 - kTile), h, kh, r0);
     const Tile<Tin> &tl = tile[buf];
-#pragma unroll 2
-    for (int t = 0; t < m; ++t) {
-      float4 k[NK], q[NK];
+    const auto load = [&](const Tin *row, float4 (&x)[NK]) {
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
         const int col = 4 * (lane8 + 8 * i);
-        k[i] = q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (col < dk) {
-          k[i] = load4(&tl.k[t][col]);
-          q[i] = load4(&tl.q[t][col]);
-        }
+        x[i] = col < dk ? load4(row + col) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      const float decay = expf(tl.la[t]);
-      float u = to_f32(tl.v[t][group]);
-      if (kGdn) {
-        float p = 0.f;
+    };
+    float4 k[NK], sp = make_float4(0.f, 0.f, 0.f, 0.f);
+    load(tl.k[0], k);
 #pragma unroll
-        for (int i = 0; i < NK; ++i) p = dot4(S[i], k[i], p);
-        u = tl.b[t] * (u - decay * sum8(p));
-      }
-      float o = 0.f;
+    for (int i = 0; i < NK; ++i) dot4(S[i], k[i], sp);
+    float p = kGdn ? sum8(sum4(sp)) : 0.f, decay = expf(tl.la[0]);
+#pragma unroll 2
+    for (int t = 0; t < m; ++t) {
+      const int next = min(t + 1, m - 1);
+      float4 q[NK], kn[NK];
+      load(tl.q[t], q);
+      load(tl.k[next], kn);
+      const float decay_next = expf(tl.la[next]);
+      float u = to_f32(tl.v[t][group]);
+      if (kGdn) u = tl.b[t] * (u - decay * p);
+      float4 so = make_float4(0.f, 0.f, 0.f, 0.f);
+      sp = so;
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
         S[i].x = fmaf(u, k[i].x, decay * S[i].x);
         S[i].y = fmaf(u, k[i].y, decay * S[i].y);
         S[i].z = fmaf(u, k[i].z, decay * S[i].z);
         S[i].w = fmaf(u, k[i].w, decay * S[i].w);
-        o = dot4(S[i], q[i], o);
+        if (kGdn) dot4(S[i], kn[i], sp);
+        dot4(S[i], q[i], so);
+        k[i] = kn[i];
       }
-      o = sum8(o);
+      const float o = sum8(sum4(so));
+      if (kGdn) p = sum8(sum4(sp));
+      decay = decay_next;
       if (lane8 == 0) o_tile[buf][t][group] = o;
     }
     __syncthreads();

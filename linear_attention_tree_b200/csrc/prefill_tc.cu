@@ -13,8 +13,9 @@
 // Precision.  States are fp32 and every product on their path is as good: a bf16 operand (k, q)
 // meets an fp32 one cut into three bf16 pieces of 8 bits (exact), T and R meet as pairs of tf32
 // (22 bits; the product of the two low parts, 2^-22 and less, is left out).  The output's own
-// products use two pieces (16 bits) where out is bf16 and all three where it is fp32.  Decay
-// ratios are powers of two of a difference of sums kept as an fp32 pair.
+// products are as good where out is fp32.  Where it is bf16 (2^-8), S Q^T takes two pieces of S
+// (16 bits) and U P^T is one tf32 product (11 bits).  Decay ratios are powers of two of a
+// difference of sums kept as an fp32 pair.
 //
 // One CTA of 13 warps per (sequence, head), one per SM.  The chain of a chunk is
 //     S -> [S K^T] -> R -> [R T^T] -> U -> [U~ K] -> S'          ([..] tensor core),
@@ -23,7 +24,7 @@
 //               its pieces into tensor memory; gamma S q scaled, the previous chunk's o stored.
 //   warps 8-11  the next chunk's gates, Gram blocks [Q;K] K^T, T (16 x 16 diagonal blocks by
 //               substitution, the rest by block products) and P, into operand tiles.
-//   warp 12     one thread issues the copies (TMA, two q / k / v buffers) and the MMAs:
+//   warp 12     one lane issues the copies (TMA, two q / k / v buffers) and the MMAs:
 //               S K^T, the next Gram block, R T^T, S Q^T, U~ K, U P^T.
 // Tensor memory (512 columns): [0,192) the pieces of S, D = U~ K over [0,128); [192,256) S K^T,
 // then U, then low pieces of U; [256,320) S Q^T, then o; [320,448) R as two tf32 halves, then the
@@ -58,13 +59,16 @@ constexpr int kTileBytes = 2 * kHalf + 2 * kVHalf;      // q, k, v of a chunk: 4
 constexpr int kOffV = 2 * kHalf;
 constexpr int kOffT = 2 * kTileBytes;        // T: high and low tf32, each two atoms of 32 columns
 constexpr int kTAtom = kC * 128;
-constexpr int kOffP = kOffT + 4 * kTAtom;    // P: three bf16 pieces
-constexpr int kPBytes = kC * 128;
-constexpr int kOffMeta = kOffP + 3 * kPBytes;
+constexpr int kPPart = kC * 128;             // P, two buffers: three bf16 pieces, or two tf32 atoms
+constexpr int kPBytes = 3 * kPPart;
+constexpr int kOffP = kOffT + 4 * kTAtom;
+constexpr int kOffMeta = kOffP + 2 * kPBytes;
 constexpr int kLd = 68;                      // row of the fp32 work matrices
 
 struct Gates {
-  float clh[kC], cll[kC];                    // cl in powers of two, as a pair
+  __align__(16) float clh[kC];               // cl in powers of two, as a pair
+  float cll[kC];
+  float end[kC];                             // exp(cl at the end of the block of 16 - cl)
   float gam[kC], bg[kC], bq[kC], tail[kC];   // gamma, b gamma, b, exp(cl_last - cl)
   float g;                                   // gamma of the last token
 };
@@ -82,7 +86,7 @@ struct Meta {
   int fail;
   __align__(16) float L[kC][kLd];
   __align__(16) float T[kC][kLd];
-  float X[4][16][20];
+  float X[4][16][20];                        // scratch of the preparing warps
   Gates gate[4];
 };
 constexpr int kSmemBytes = kOffMeta + (int)sizeof(Meta) + 1024;
@@ -115,11 +119,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&r)[32]) {
   for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
 }
 
-// x (two values, 2 i and 2 i + 1) cut into bf16 pieces of 8 bits each, packed; exact together.
+// Two values cut: the packed upper halves (a bf16 piece each), leaving what is left of the values.
+// Three pieces hold a value exactly.
 __device__ __forceinline__ uint32_t cut(float &x0, float &x1) {
   const uint32_t a = __float_as_uint(x0), b = __float_as_uint(x1);
-  x0 -= __uint_as_float(a & 0xFFFF0000u);
-  x1 -= __uint_as_float(b & 0xFFFF0000u);
+  const uint32_t na = (a & 0xFFFF0000u) ^ 0x80000000u, nb = (b & 0xFFFF0000u) ^ 0x80000000u;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "r"(na), "r"(nb));
   return __byte_perm(a, b, 0x7632);
 }
 // 32 values into kN pieces of 16 columns each, at col, col + step, ...
@@ -177,32 +186,82 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// acc[r] += rows row0 + r of A times column `col` of B, 16 x 16 blocks with rows of kLd (or ldb).
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float both(uint64_t a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+  return x + y;
+}
+
+// acc[r] += row row0 + r of A times column `col` of B for 16 x 16 blocks: even and odd products in
+// the halves of a packed pair.
 template <int R>
-__device__ __forceinline__ void block_product(float (&acc)[R], const float *A, int row0, const float *B,
+__device__ __forceinline__ void block_product(uint64_t (&acc)[R], const float *A, int row0, const float *B,
                                               int ldb, int col) {
 #pragma unroll
   for (int k = 0; k < 16; k += 4) {
-    float b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = B[(k + i) * ldb + col];
+    const uint64_t b0 = pair(B[k * ldb + col], B[(k + 1) * ldb + col]);
+    const uint64_t b1 = pair(B[(k + 2) * ldb + col], B[(k + 3) * ldb + col]);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float4 a = *reinterpret_cast<const float4 *>(A + (row0 + r) * kLd + k);
-      acc[r] = fmaf(a.x, b[0], fmaf(a.y, b[1], fmaf(a.z, b[2], fmaf(a.w, b[3], acc[r]))));
+      acc[r] = fma2(pair(a.x, a.y), b0, fma2(pair(a.z, a.w), b1, acc[r]));
     }
   }
 }
 
-// T = (I + L)^-1 for the unit lower triangular system in mt.L, by the preparing warps.
-__device__ __forceinline__ void invert(Meta &mt, int aw, int lane) {
-  const int col = lane & 15, grp = lane >> 4;
-  const auto Lb = [&](int i, int j) { return &mt.L[16 * i][16 * j]; };
-  const auto Tb = [&](int i, int j) { return &mt.T[16 * i][16 * j]; };
+// T[row][i] into the operand tiles (high and low tf32).
+__device__ __forceinline__ void put_t(unsigned char *sm, int row, int i, float t) {
+  const int at = kOffT + (i >> 5) * kTAtom + row * 128 + ((((i >> 2) & 7) ^ (row & 7)) << 4) + (i & 3) * 4;
+  const float hi = tf32_round(t);
+  *reinterpret_cast<float *>(sm + at) = hi;
+  *reinterpret_cast<float *>(sm + at + 2 * kTAtom) = t - hi;
+}
+
+// Blocks (J + 1 .. 3, J) of T, a warp's kCols columns of them: T_iJ = -T_ii sum_k L_ik T_kJ.  Columns
+// of blocks do not depend on one another once the diagonal is there.
+template <int kCols>
+__device__ __forceinline__ void solve_columns(Meta &mt, unsigned char *sm, int J, int col0, int lane,
+                                              float (*X)[20]) {
+  constexpr int R = kCols / 2;                   // 32 / kCols groups of lanes share 16 rows
+  const int col = col0 + (lane & (kCols - 1)), row = (lane / kCols) * R;
+  for (int i = J + 1; i < 4; ++i) {
+    uint64_t acc[R] = {};
+    for (int k = J; k < i; ++k)
+      block_product<R>(acc, &mt.L[16 * i][16 * k], row, &mt.T[16 * k][16 * J], kLd, col);
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r) X[row + r][col] = both(acc[r]);
+    __syncwarp();
+    uint64_t out[R] = {};
+    block_product<R>(out, &mt.T[16 * i][16 * i], row, &X[0][0], 20, col);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float t = -both(out[r]);
+      if (i < 3) mt.T[16 * i + row + r][16 * J + col] = t;
+      put_t(sm, 16 * i + row + r, 16 * J + col, t);
+    }
+    __syncwarp();
+  }
+}
+
+// T = (I + L)^-1 for the unit lower triangular system in mt.L, into the operand tiles, by the
+// preparing warps: the four diagonal blocks by substitution, then two warps take the first column
+// of blocks (nine products of 16 x 16 blocks in all), one the second (five), one the third (two).
+__device__ __forceinline__ void invert(Meta &mt, unsigned char *sm, int aw, int lane) {
   {
-    // diagonal block aw: lane `col` solves for its column
+    const int col = lane & 15, half = lane >> 4;
     float x[16];
-    const float *D = Lb(aw, aw);
+    const float *D = &mt.L[16 * aw][16 * aw];
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
       float s[4] = {n == col ? 1.f : 0.f, 0.f, 0.f, 0.f};
@@ -216,56 +275,25 @@ __device__ __forceinline__ void invert(Meta &mt, int aw, int lane) {
       }
       x[n] = (s[0] + s[1]) + (s[2] + s[3]);
     }
-    if (grp == 0) {
+    // both halves hold the column: each writes every other row
 #pragma unroll
-      for (int n = 0; n < 16; ++n) Tb(aw, aw)[n * kLd + col] = x[n];
+    for (int n = 0; n < 16; n += 2) {
+      const int row = 16 * aw + n + half, i = 16 * aw + col;
+      const float t = half ? x[n + 1] : x[n];
+      mt.T[row][i] = t;
+      put_t(sm, row, i, t);
     }
   }
   group_sync(2, kPrep * 32);
-  if (aw < 3) {
-    // block (aw + 1, aw): -T L T
-    float acc[8] = {};
-    block_product<8>(acc, Lb(aw + 1, aw), 8 * grp, Tb(aw, aw), kLd, col);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) mt.X[aw][8 * grp + r][col] = acc[r];
-    __syncwarp();
-    float out[8] = {};
-    block_product<8>(out, Tb(aw + 1, aw + 1), 8 * grp, &mt.X[aw][0][0], 20, col);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) Tb(aw + 1, aw)[(8 * grp + r) * kLd + col] = -out[r];
-  }
-  group_sync(2, kPrep * 32);
-  {
-    // blocks (2, 0) and (3, 1), two warps each
-    const int j = aw >> 1, i = j + 2, row = 8 * (aw & 1) + 4 * grp;
-    float acc[4] = {};
-    block_product<4>(acc, Lb(i, j), row, Tb(j, j), kLd, col);
-    block_product<4>(acc, Lb(i, j + 1), row, Tb(j + 1, j), kLd, col);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) mt.X[j][row + r][col] = acc[r];
-    group_sync(2, kPrep * 32);
-    float out[4] = {};
-    block_product<4>(out, Tb(i, i), row, &mt.X[j][0][0], 20, col);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) Tb(i, j)[(row + r) * kLd + col] = -out[r];
-  }
-  group_sync(2, kPrep * 32);
-  {
-    // block (3, 0), four rows a warp
-    const int row = 4 * aw + 2 * grp;
-    float acc[2] = {};
-    block_product<2>(acc, Lb(3, 0), row, Tb(0, 0), kLd, col);
-    block_product<2>(acc, Lb(3, 1), row, Tb(1, 0), kLd, col);
-    block_product<2>(acc, Lb(3, 2), row, Tb(2, 0), kLd, col);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) mt.X[2][row + r][col] = acc[r];
-    group_sync(2, kPrep * 32);
-    float out[2] = {};
-    block_product<2>(out, Tb(3, 3), row, &mt.X[2][0][0], 20, col);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) Tb(3, 0)[(row + r) * kLd + col] = -out[r];
-  }
-  group_sync(2, kPrep * 32);
+  if (aw < 2) solve_columns<8>(mt, sm, 0, 8 * aw, lane, mt.X[aw]);
+  else solve_columns<16>(mt, sm, aw - 1, 0, lane, mt.X[aw]);
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 template <bool kGdn, typename Tout>
@@ -397,17 +425,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) u[j] = value(32 * hf + j);
       }
-      // pieces of U~ (decayed to the chunk's end) and of U
+      // pieces of U~ (decayed to the chunk's end), and U for the output
       {
         float x[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] = u[j] * gt.tail[32 * hf + j];
         store_pieces<3>(tl + kColUt + 16 * hf, 32, x);
-        float packed[16];
+        if (kNO == 3) {
+          float packed[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) packed[i] = __uint_as_float(cut(u[2 * i], u[2 * i + 1]));
-        ptx::tmem_st16(tl + kColU + 16 * hf, packed);
-        store_pieces<kNO - 1>(tl + kColSK + 32 * hf, 16, u);
+          for (int i = 0; i < 16; ++i) packed[i] = __uint_as_float(cut(u[2 * i], u[2 * i + 1]));
+          ptx::tmem_st16(tl + kColU + 16 * hf, packed);
+          store_pieces<2>(tl + kColSK + 32 * hf, 16, u);
+        } else {
+          // U in tf32, over the accumulator it came from
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float y[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = tf32_round(u[16 * g + j]);
+            ptx::tmem_st16(tl + kColSK + 32 * hf + 16 * g, y);
+          }
+        }
       }
       ptx::tmem_wait_st();
       sy.arrive_tmem(kU);
@@ -468,6 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     if (aw == 0) fetch(0);
+    // blocks above the diagonal of T stay zero
+    for (int e = aw * 32 + lane; e < 4 * kTAtom / 16; e += kPrep * 32)
+      *reinterpret_cast<uint4 *>(sm + kOffT + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+    group_sync(2, kPrep * 32);
     for (int c = 0; c < chunks; ++c) {
       Gates &gt = mt.gate[c & 3];
       unsigned char *tile = sm + (c & 1) * kTileBytes;
@@ -506,6 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           gt.bg[i] = bb[e] * gam;
           gt.bq[i] = bb[e];
           gt.tail[i] = exp2f((float)(all - cl));
+          const double end = __shfl_sync(0xffffffffu, sum, lane | 7);
+          gt.end[i] = exp2f((float)(end - cl));
         }
         if (lane == 31) gt.g = exp2f((float)all);
         sy.arrive_warp(kGates0 + (c & 1));
@@ -526,106 +571,131 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 32; ++i) x[32 + i] = g0[i];
       }
       sy.arrive_tmem(kGramFree);
+      // decay ratios: inside a diagonal block of 16 one by one; before it as the product of
+      // exp(cl_row - cl at the end of the column's block) and gate `end` of the column (both at
+      // most 1 for decays)
       const float clh = gt.clh[row], cll = gt.cll[row];
       const bool is_k = aw >= 2;
       const float scale = is_k ? gt.bq[row] : 1.f;
       const int last = is_k ? row - 1 : row;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const float d = (clh - gt.clh[i]) + (cll - gt.cll[i]);
-        x[i] = i <= last ? scale * pow2(d) * x[i] : 0.f;
+      for (int J = 0; J < 4; ++J) {
+        const float before = scale * pow2((clh - gt.clh[16 * J + 15]) + (cll - gt.cll[16 * J + 15]));
+        const bool diagonal = J >> 1 == (aw & 1);        // of some of the warp's rows
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const int i = 16 * J + j;
+          const float4 end = *reinterpret_cast<const float4 *>(&gt.end[i]);
+          float f[4] = {before * end.x, before * end.y, before * end.z, before * end.w};
+          if (diagonal) {
+            const float4 ch = *reinterpret_cast<const float4 *>(&gt.clh[i]);
+            const float4 cl = *reinterpret_cast<const float4 *>(&gt.cll[i]);
+            const float d[4] = {(clh - ch.x) + (cll - cl.x), (clh - ch.y) + (cll - cl.y),
+                                (clh - ch.z) + (cll - cl.z), (clh - ch.w) + (cll - cl.w)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (J == row >> 4) f[e] = scale * pow2(d[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i + e] = i + e <= last ? f[e] * x[i + e] : 0.f;
+        }
+      }
+      if (!is_k) {
+        // P into its operand (the buffer's last reader was chunk c - 2, before this chunk's tile)
+        unsigned char *pt = sm + kOffP + (c & 1) * kPBytes + row * 128;
+        if (kNO == 3) {
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint4 w;
+              w.x = cut(x[8 * j], x[8 * j + 1]);
+              w.y = cut(x[8 * j + 2], x[8 * j + 3]);
+              w.z = cut(x[8 * j + 4], x[8 * j + 5]);
+              w.w = cut(x[8 * j + 6], x[8 * j + 7]);
+              *reinterpret_cast<uint4 *>(pt + p * kPPart + ((j ^ (row & 7)) << 4)) = w;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            *reinterpret_cast<float4 *>(pt + (j >> 3) * kPPart + (((j & 7) ^ (row & 7)) << 4)) =
+                make_float4(tf32_round(x[4 * j]), tf32_round(x[4 * j + 1]), tf32_round(x[4 * j + 2]),
+                            tf32_round(x[4 * j + 3]));
+        }
+      } else if (kGdn) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4)
+          *reinterpret_cast<float4 *>(&mt.L[row][i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
       }
       if (kGdn) {
-        if (is_k) {
-#pragma unroll
-          for (int i = 0; i < 64; i += 4)
-            *reinterpret_cast<float4 *>(&mt.L[row][i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        }
         group_sync(2, kPrep * 32);
-        invert(mt, aw, lane);
-        // T into its operand: two threads a row, 32 columns (one atom) each
-        if (c > 0) sy.wait(kTR, c - 1);
-        const int r = (32 * aw + lane) >> 1, atom = lane & 1;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float4 t = *reinterpret_cast<const float4 *>(&mt.T[r][32 * atom + 4 * j]);
-          // blocks above the diagonal are never written in mt.T
-          if ((32 * atom + 4 * j) >> 4 > r >> 4) t = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4 hi = make_float4(tf32_round(t.x), tf32_round(t.y), tf32_round(t.z), tf32_round(t.w));
-          const int at = kOffT + atom * kTAtom + r * 128 + ((j ^ (r & 7)) << 4);
-          *reinterpret_cast<float4 *>(sm + at) = hi;
-          *reinterpret_cast<float4 *>(sm + at + 2 * kTAtom) =
-              make_float4(t.x - hi.x, t.y - hi.y, t.z - hi.z, t.w - hi.w);
-        }
-      }
-      // P into its pieces
-      if (!is_k) {
-        if (c > 0) sy.wait(kO, c - 1);
-#pragma unroll
-        for (int p = 0; p < kNO; ++p) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint4 w;
-            w.x = cut(x[8 * j], x[8 * j + 1]);
-            w.y = cut(x[8 * j + 2], x[8 * j + 3]);
-            w.z = cut(x[8 * j + 4], x[8 * j + 5]);
-            w.w = cut(x[8 * j + 6], x[8 * j + 7]);
-            *reinterpret_cast<uint4 *>(sm + kOffP + p * kPBytes + row * 128 + ((j ^ (row & 7)) << 4)) = w;
-          }
-        }
+        if (c > 0) sy.wait(kTR, c - 1);            // T of the chunk before has been read
+        invert(mt, sm, aw, lane);
       }
       ptx::fence_proxy_async_smem();
       sy.arrive_warp(kPrepared);
     }
-  } else if (lane == 0) {
-    // ==== copies and MMAs ========================================================================
-    ptx::prefetch_tmap(&tm_q);
-    ptx::prefetch_tmap(&tm_k);
-    ptx::prefetch_tmap(&tm_v);
+  } else {
+    // ==== copies and MMAs: the warp goes through the waits together, one lane issues ============
+    const bool one = elect_one();
+    if (one) {
+      ptx::prefetch_tmap(&tm_q);
+      ptx::prefetch_tmap(&tm_k);
+      ptx::prefetch_tmap(&tm_v);
+    }
     int loaded = 0;
     const auto load = [&](int c) {
       const uint32_t b = sbase + (c & 1) * kTileBytes, bar = sy.at(kFull0 + (c & 1));
-      ptx::mbar_arrive_expect_tx(bar, kTileBytes);
+      if (one) {
+        ptx::mbar_arrive_expect_tx(bar, kTileBytes);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        ptx::tma_load_3d(b + half * kHalf + kKRow, &tm_k, bar, half * 64, kh, lo + c * kC);
-        ptx::tma_load_3d(b + half * kHalf, &tm_q, bar, half * 64, kh, lo + c * kC);
-        ptx::tma_load_3d(b + kOffV + half * kVHalf, &tm_v, bar, half * 64, h, lo + c * kC);
+        for (int half = 0; half < 2; ++half) {
+          ptx::tma_load_3d(b + half * kHalf + kKRow, &tm_k, bar, half * 64, kh, lo + c * kC);
+          ptx::tma_load_3d(b + half * kHalf, &tm_q, bar, half * 64, kh, lo + c * kC);
+          ptx::tma_load_3d(b + kOffV + half * kVHalf, &tm_v, bar, half * 64, h, lo + c * kC);
+        }
       }
       loaded = c + 1;
     };
     constexpr uint32_t kId64 = ptx::idesc_bf16_f32(128, 64), kId128 = ptx::idesc_bf16_f32(128, 128);
     constexpr uint32_t kIdT = ptx::idesc_tf32_f32(128, 64);
-    // K-major operand of 64-column halves `half` bytes apart, step kk of 16 columns
-    const auto step = [](uint32_t base, int half, int kk) {
-      return ptx::smem_desc_sw128(base + (kk >> 2) * half + (kk & 3) * 32, 1024);
-    };
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    // descriptors of the operands at their first step; a step adds its offset in 16 bytes
+    const uint64_t d_qk = ptx::smem_desc_sw128(sbase, 1024);
+    const uint64_t d_kn = desc_n_major(sbase + kKRow, kHalf, 1024);
+    const uint64_t d_t = ptx::smem_desc_sw128(sbase + kOffT, 1024);
+    const uint64_t d_p = ptx::smem_desc_sw128(sbase + kOffP, 1024);
+    // step kk of a K-major operand in columns of 128 bytes `half` bytes apart
+    const auto step = [](int half, int kk) { return (uint64_t)(((kk >> 2) * half + (kk & 3) * 32) >> 4); };
     const auto gram = [&](int c) {
-      const uint32_t b = sbase + (c & 1) * kTileBytes;
+      const uint64_t q = d_qk + ((c & 1) * kTileBytes >> 4), k = q + (kKRow >> 4);
+      if (one) {
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        ptx::mma_bf16(tmem + kColG, step(b, kHalf, kk), step(b + kKRow, kHalf, kk), kId64, kk > 0);
-      ptx::mma_commit(sy.at(kGram));
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::mma_bf16(tm + kColG, q + step(kHalf, kk), k + step(kHalf, kk), kId64, kk > 0);
+        ptx::mma_commit(sy.at(kGram));
+      }
     };
     bool ok = true;
     load(0);
     if (chunks > 1) load(1);
     if ((ok = sy.wait(kTile, 0))) gram(0);
     for (int c = 0; ok && c < chunks; ++c) {
-      const uint32_t b = sbase + (c & 1) * kTileBytes;
+      const uint64_t q = d_qk + ((c & 1) * kTileBytes >> 4), k = q + (kKRow >> 4);
       // S in pieces; by then the chunk before is through with its tiles and its operands
       if (!(ok = sy.wait(kS, c) && (c == 0 || sy.wait(kO, c - 1)))) break;
       ptx::tc_fence_after();
-      if (c > 0 && c + 1 < chunks) load(c + 1);
-      if (kGdn) {
+      if (kGdn && one) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
           for (int p = 0; p < 3; ++p)
-            ptx::mma_bf16_tmem_a(tmem + kColSK, tmem + kColS + 64 * p + 8 * kk, step(b + kKRow, kHalf, kk),
-                                 kId64, kk + p > 0);
+            ptx::mma_bf16_tmem_a(tm + kColSK, tm + kColS + 64 * p + 8 * kk, k + step(kHalf, kk), kId64,
+                                 kk + p > 0);
         ptx::mma_commit(sy.at(kSK));
       }
+      if (c > 0 && c + 1 < chunks) load(c + 1);
       if (c + 1 < chunks) {
         if (!(ok = sy.wait(kTile, c + 1) && sy.wait(kGramFree, c))) break;
         ptx::tc_fence_after();
@@ -635,55 +705,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kGdn) {
         if (!(ok = sy.wait(kR, c))) break;
         ptx::tc_fence_after();
+        if (one) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t hi = step(sbase + kOffT, kTAtom, kk);
-          const uint64_t low = step(sbase + kOffT + 2 * kTAtom, kTAtom, kk);
-          ptx::mma_tf32_tmem_a(tmem + kColSK, tmem + kColR + 8 * kk, hi, kIdT, kk > 0);
-          ptx::mma_tf32_tmem_a(tmem + kColSK, tmem + kColR + 8 * kk, low, kIdT, 1);
-          ptx::mma_tf32_tmem_a(tmem + kColSK, tmem + kColR + 64 + 8 * kk, hi, kIdT, 1);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t hi = d_t + step(kTAtom, kk), low = hi + (2 * kTAtom >> 4);
+            ptx::mma_tf32_tmem_a(tm + kColSK, tm + kColR + 8 * kk, hi, kIdT, kk > 0);
+            ptx::mma_tf32_tmem_a(tm + kColSK, tm + kColR + 8 * kk, low, kIdT, 1);
+            ptx::mma_tf32_tmem_a(tm + kColSK, tm + kColR + 64 + 8 * kk, hi, kIdT, 1);
+          }
+          ptx::mma_commit(sy.at(kTR));
         }
-        ptx::mma_commit(sy.at(kTR));
       }
       if (c > 0 && !(ok = sy.wait(kOFree, c - 1))) break;
       ptx::tc_fence_after();
+      if (one) {
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
+        for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
-        for (int p = 0; p < kNO; ++p)
-          ptx::mma_bf16_tmem_a(tmem + kColO, tmem + kColS + 64 * p + 8 * kk, step(b, kHalf, kk), kId64,
-                               kk + p > 0);
-      ptx::mma_commit(sy.at(kSQ));
+          for (int p = 0; p < kNO; ++p)
+            ptx::mma_bf16_tmem_a(tm + kColO, tm + kColS + 64 * p + 8 * kk, q + step(kHalf, kk), kId64,
+                                 kk + p > 0);
+        ptx::mma_commit(sy.at(kSQ));
+      }
       // U~ K over the columns of S, which S Q^T must have read
       if (!(ok = sy.wait(kU, c) && sy.wait(kSQ, c))) break;
       ptx::tc_fence_after();
+      if (one) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint64_t kd = desc_n_major(b + kKRow + kk * 2048, kHalf, 1024);
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t kd = d_kn + ((c & 1) * kTileBytes >> 4) + (kk * 2048 >> 4);
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-          ptx::mma_bf16_tmem_a(tmem + kColD, tmem + kColUt + 32 * p + 8 * kk, kd, kId128 | kBTransposed,
-                               kk + p > 0);
+          for (int p = 0; p < 3; ++p)
+            ptx::mma_bf16_tmem_a(tm + kColD, tm + kColUt + 32 * p + 8 * kk, kd, kId128 | kBTransposed,
+                                 kk + p > 0);
+        }
+        ptx::mma_commit(sy.at(kD));
       }
-      ptx::mma_commit(sy.at(kD));
       if (!(ok = sy.wait(kScaled, c))) break;
       ptx::tc_fence_after();
+      if (one) {
+        const uint64_t pd = d_p + ((c & 1) * kPBytes >> 4);
+        if (kNO == 3) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        // piece p of U at its columns, piece r of P
+          for (int kk = 0; kk < 4; ++kk) {
+            // piece p of U at its columns, piece r of P
 #pragma unroll
-        for (int p = 0; p < kNO; ++p) {
-          const uint32_t up = p == 0 ? kColU + 8 * kk : kColSK + 32 * (kk >> 1) + 16 * (p - 1) + 8 * (kk & 1);
+            for (int p = 0; p < 3; ++p) {
+              const uint32_t up =
+                  p == 0 ? kColU + 8 * kk : kColSK + 32 * (kk >> 1) + 16 * (p - 1) + 8 * (kk & 1);
 #pragma unroll
-          for (int r = 0; r < kNO - p; ++r)
-            ptx::mma_bf16_tmem_a(tmem + kColO, tmem + up,
-                                 ptx::smem_desc_sw128(sbase + kOffP + r * kPBytes + kk * 32, 1024), kId64, 1);
+              for (int r = 0; r < 3 - p; ++r)
+                ptx::mma_bf16_tmem_a(tm + kColO, tm + up, pd + ((r * kPPart + kk * 32) >> 4), kId64, 1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            ptx::mma_tf32_tmem_a(tm + kColO, tm + kColSK + 8 * kk, pd + step(kPPart, kk), kIdT, 1);
         }
+        ptx::mma_commit(sy.at(kO));
       }
-      ptx::mma_commit(sy.at(kO));
     }
     // what was issued has to end before the CTA does
-    ptx::mma_commit(sy.at(kEnd));
+    if (one) ptx::mma_commit(sy.at(kEnd));
     ptx::mbar_wait_bounded(sy.at(kEnd), 0, kSpinLimit);
     for (int c = loaded > 2 ? loaded - 2 : 0; c < loaded; ++c)
       ptx::mbar_wait_bounded(sy.at(kFull0 + (c & 1)), (c >> 1) & 1, kSpinLimit);
