@@ -33,6 +33,15 @@ tv_status check_sequence(const tv_problem *p) {
   return TV_OK;
 }
 
+// Shapes of the tensor-core prefill, and whether it is the one that runs.
+bool prefill_tc_takes(const tv_problem *p) {
+  return p->in_dtype == TV_BF16 && p->dk == 128 && p->dv == 128 &&
+         (p->total_nodes / 64 + (long long)p->B) * p->H <= 0x7fffffffLL;
+}
+bool prefill_on_tc(const tv_problem *p) {
+  return p->total_nodes > 0 && p->B > 0 && p->kernel != TV_KERNEL_SIMT && prefill_tc_takes(p);
+}
+
 // S_out either is S_in or does not overlap it.
 bool states_apart(const tv_problem *p, const float *S_in, const float *S_out) {
   const size_t bytes = (size_t)p->B * p->H * p->dv * p->dk * sizeof(float);
@@ -63,7 +72,8 @@ tv_status check_sample(const tv_sample_problem *p) {
 extern "C" {
 
 size_t tv_prefill_workspace_size(const tv_problem *p) {
-  return check_sequence(p) == TV_OK ? kWorkspaceBytes : 0;
+  if (check_sequence(p) != TV_OK) return 0;
+  return prefill_on_tc(p) ? prefill_tc_workspace(p->total_nodes, p->B, p->H, p->mode) : kWorkspaceBytes;
 }
 
 tv_status tv_prefill(const tv_problem *p, const void *q, const void *k, const void *v,
@@ -77,13 +87,12 @@ tv_status tv_prefill(const tv_problem *p, const void *q, const void *k, const vo
       !arr(seq_offsets, false) || !opt(S_in) || !arr(S_out, p->B == 0) || !arr(workspace, false))
     return TV_ERR_INVALID_ARG;
   if (p->mode == TV_MODE_GDN ? !arr(b, none) : !opt(b)) return TV_ERR_INVALID_ARG;
-  if (workspace_bytes < tv_prefill_workspace_size(p)) return TV_ERR_INVALID_ARG;
   if (!states_apart(p, S_in, S_out)) return TV_ERR_INVALID_ARG;
-  const bool tc = p->in_dtype == TV_BF16 && p->dk == 128 && p->dv == 128;
-  if (p->kernel == TV_KERNEL_TC && !tc) return TV_ERR_UNSUPPORTED;
+  if (p->kernel == TV_KERNEL_TC && !prefill_tc_takes(p)) return TV_ERR_UNSUPPORTED;
+  if (workspace_bytes < tv_prefill_workspace_size(p)) return TV_ERR_INVALID_ARG;
   if (p->B == 0) return TV_OK;
   const SequenceArgs a = sequence_args(p, q, k, v, log_a, b, seq_offsets, S_in, out, S_out, workspace);
-  if (tc && !none && p->kernel != TV_KERNEL_SIMT)
+  if (prefill_on_tc(p))
     return record_cuda_error(
         launch_prefill_tc(a, p->mode, p->out_dtype, reinterpret_cast<cudaStream_t>(stream)));
   return record_cuda_error(launch_prefill_simt(a, p->mode, p->in_dtype, p->out_dtype,

@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(kThreads) prefill_kernel(SequenceArgs a) {
   const int s = item / H, h = item % H, kh = qk_head(h, H, a.Hk);
   const int lane8 = threadIdx.x & 7, group = threadIdx.x >> 3;
   int lo, n;
-  if (!sequence_range(a.offsets, s, a.T, a.max_len, lo, n)) {
+  const bool in = sequence_range(a.offsets, s, a.T, a.max_len, lo, n);
+  if (!__syncthreads_and(in && sequence_rises(a.offsets, s, lo, threadIdx.x, kThreads))) {
     if (threadIdx.x == 0) set_status(a.ws, TV_ERR_BAD_TREE, s);
     return;
   }

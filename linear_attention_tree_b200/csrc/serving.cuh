@@ -46,8 +46,18 @@ __device__ __forceinline__ bool sequence_range(const int32_t *offsets, int s, in
   return lo >= 0 && hi >= lo && hi <= T && n <= max_len;
 }
 
+// Whether no offset up to sequence s is larger than its start, as far as threads tid, tid + step, ...
+// see: sequences then never share rows or a place in the workspace.
+__device__ __forceinline__ bool sequence_rises(const int32_t *offsets, int s, int lo, int tid, int step) {
+  bool ok = true;
+  for (int i = tid; i < s; i += step) ok &= offsets[i] <= lo;
+  return ok;
+}
+
 cudaError_t launch_prefill_simt(const SequenceArgs &a, int mode, int in_dtype, int out_dtype,
                                 cudaStream_t st);
+size_t prefill_tc_workspace(long long T, long long B, long long H, int mode);
+cudaError_t launch_prefill_prepare(const SequenceArgs &a, int mode, cudaStream_t st);
 cudaError_t launch_prefill_tc(const SequenceArgs &a, int mode, int out_dtype, cudaStream_t st);
 cudaError_t launch_decode_step(const SequenceArgs &a, int mode, int in_dtype, int out_dtype,
                                cudaStream_t st);
