@@ -282,10 +282,13 @@ TV_API tv_status tv_snapshot_commit(const tv_problem *p, const float *snapshots,
  *   out        [T][H][dv] out_dtype                                     (device, written)
  *   S_out      [B][H][dv][dk] fp32; may be S_in itself, must not partially overlap it
  *                                                                       (device, written)
- *   workspace  tv_prefill_workspace_size(p) bytes, as for trees.  Calls that may run at the
- *              same time need a workspace each.
- * A sequence whose range is not inside [0, T] or is longer than max_nodes records
- * TV_ERR_BAD_TREE and is left unwritten. */
+ *   workspace  tv_prefill_workspace_size(p) bytes, as for trees: the status word alone, or, for
+ *              the tensor-core kernel (bf16, dk = dv = 128; AUTO takes it for long or many
+ *              sequences), 20 KiB (10 KiB in scalar mode) for each chunk of 64 tokens and head,
+ *              (T / 64 + B) * H in all.  Calls that may run at the same time, replays of
+ *              captured ones too, need a workspace each.
+ * A sequence whose range is not inside [0, T], is longer than max_nodes, or starts before an
+ * earlier offset (they have to rise) records TV_ERR_BAD_TREE and is left unwritten. */
 TV_API size_t tv_prefill_workspace_size(const tv_problem *p);
 TV_API tv_status tv_prefill(const tv_problem *p, const void *q, const void *k, const void *v,
                             const float *log_a, const float *b, const int32_t *seq_offsets,
