@@ -24,6 +24,11 @@
 //                  their range of logits (for 16-bit logits, or such widened to 32: one part
 //                  per value, and the border is known), and a fourth read does the rest.
 //   otherwise      a second read sums the kept weights by segments.
+//   bf16 logits    (top-p and otherwise) take few values: those of a magnitude from 2^-8 to 2^8 have
+//                  a counter and a weight each in shared memory, so a weight is computed once for
+//                  a value (4096 of them) and not for a logit, top-p's border is known from the
+//                  counts alone, and the sums by segments look weights up.  The few others go by
+//                  the exponential.
 // The segment that holds the token is then read once more.  Where a list overflows or top-k is
 // large, the border comes from a radix descent over the logits' bits (slow and general).
 // Second and later reads hit L2.
@@ -101,6 +106,23 @@ struct Weigher {
     return in ? __hiloint2double(__double2hiint(w) + ((i >> 4) << 20), __double2loint(w)) : 0.0;
   }
 };
+
+// Values of bf16 logits with a place of their own: magnitudes from 2^-8 up to 2^8, 128 to an octave.
+constexpr int kValues = 4096;
+struct ValueSmem {
+  double w[kValues];
+  unsigned count[kValues];
+};
+constexpr uint32_t kFirstMagnitude = 0x3B80u;  // 2^-8
+// Place of the logit with these 16 bits: its magnitude's, and 2048 more for negative ones; at least
+// kValues for those without one.
+__device__ __forceinline__ uint32_t place_of(uint32_t bits) {
+  const uint32_t n = (bits & 0x7FFFu) - kFirstMagnitude;
+  return n < 2048u ? n | (bits & 0x8000u) >> 4 : kValues;
+}
+__device__ __forceinline__ float value_at(int place) {
+  return __uint_as_float((kFirstMagnitude + (place & 2047)) << 16 | (uint32_t)(place & 2048) << 20);
+}
 
 // A row of logits by aligned 16-byte vectors; the first and the last may be partial.
 template <typename T> struct Row {
@@ -391,10 +413,170 @@ __device__ void descend(const Row<T> &row, const Weigher &weight, SampleSmem &sm
   n_edge = min(n, most);
 }
 
+// bf16 logits: the border of top-p and the kept weight above it in this warp's segment of vectors
+// [s0, s1), with the border's equals there, by values.  False (nothing is known) where logits without
+// a place weigh too much for it.  Called by the whole block.
+__device__ bool by_values(const Row<__nv_bfloat16> &row, const Weigher &weight, SampleSmem &sm, ValueSmem &vs,
+                          float t, float top_p, float min_p, bool border, uint32_t &edge, int &n_edge, int s0,
+                          int s1, double &kept, int &ties) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const float top = weight.max;
+  // what lies below weighs less than 2^-1000
+  const float nothing = fmaxf(__double2float_rd((double)top - 700.0 * (double)t), -3.4028234e38f);
+  constexpr int kPer = kValues / kThreads;
+  // places in falling order of their values: positive ones from the largest on, then negative ones
+  const auto place_in_order = [](int p) { return p < 2048 ? 2047 - p : p; };
+  double mass[kPer], mine = 0.0;
+  if (border) {
+    for (int i = tid; i < kValues; i += kThreads) vs.count[i] = 0;
+    if (tid == 0) {
+      sm.n = 0;
+      sm.pick = -1;
+    }
+    __syncthreads();
+    for (int vi = tid; vi < row.vectors; vi += kThreads) {
+      if (vi >= row.full0 && vi < row.full1) {
+        const uint4 r = row.raw(vi);
+        const uint32_t word[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t bits = j & 1 ? word[j / 2] >> 16 : word[j / 2] & 0xFFFFu, p = place_of(bits);
+          if (p < kValues) {
+            atomicAdd(&vs.count[p], 1u);
+          } else if (fmaxf(__uint_as_float(bits << 16), -CUDART_INF_F) >= nothing) {
+            const int at = atomicAdd(&sm.n, 1);
+            if (at < kList) sm.list[at] = entry_of(key_of(__uint_as_float(bits << 16)), row.index(vi, j));
+          }
+        }
+      } else {
+        for (int j = 0; j < 8; ++j) {
+          const int i = row.index(vi, j);
+          if (i < 0 || i >= row.V) continue;
+          const float x = fmaxf(to_f32(row.x[i]), -CUDART_INF_F);
+          const uint32_t p = place_of(__float_as_uint(x) >> 16);
+          if (p < kValues) {
+            atomicAdd(&vs.count[p], 1u);
+          } else if (x >= nothing) {
+            const int at = atomicAdd(&sm.n, 1);
+            if (at < kList) sm.list[at] = entry_of(key_of(x), i);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (sm.n > kList) return false;
+    // the listed ones: small magnitudes, all between the positive and the negative places
+    double small = 0.0;
+    bool large = false;
+    for (int i = tid; i < sm.n; i += kThreads) large |= fabsf(value_of(entry_key(sm.list[i]))) > 1.f;
+    if (__syncthreads_or(large)) return false;
+    // (summed by falling entries, so that the order of the list does not matter)
+    sort_list(sm.list, sm.sorted, sm.n);
+    __syncthreads();
+    for (int i = tid; i < sm.n; i += kThreads) small += weight(value_of(entry_key(sm.sorted[i])));
+    small = block_sum(small, sm.part);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int p = place_in_order(tid * kPer + j);
+      const unsigned n = vs.count[p];
+      const double w = n ? weight(value_at(p)) : 0.0;
+      vs.w[p] = w;
+      mass[j] = n * w;
+      mine += mass[j];
+    }
+    double c, all;
+    int unused, unused_all;
+    block_scan(mine, 0, sm, c, unused, all, unused_all);
+    all += small;
+    if (tid * kPer >= 2048) c += small;
+    const double goal = (double)top_p * all;
+    // the last value that starts below the goal
+    int last = -1;
+    double start = 0.0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (mass[j] > 0.0 && c < goal) {
+        last = tid * kPer + j;
+        start = c;
+      }
+      c += mass[j];
+    }
+    const int warp_last = __reduce_max_sync(kFull, last);
+    if (lane == 0) atomicMax(&sm.pick, warp_last);
+    __syncthreads();
+    const int pick = sm.pick;
+    if (pick >= 0 && pick == last) {
+      const int p = place_in_order(pick), n = (int)vs.count[p];
+      const double d = (goal - start) / vs.w[p];
+      // (0: the goal lies behind this value's equals, among the small magnitudes)
+      sm.ties_left = d <= (double)n ? max(1, (int)ceil(d)) : sm.n == 0 ? n : 0;
+    }
+    __syncthreads();
+    if (pick < 0 || sm.ties_left == 0) return false;
+    edge = key_of(value_at(place_in_order(pick)));
+    n_edge = sm.ties_left;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int p = place_in_order(tid * kPer + j);
+      const float x = value_at(p);
+      vs.w[p] = x <= top ? weight(x) : 0.0;
+    }
+  }
+  // what is kept: values above the border and heavy enough; its equals are counted apart
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int p = place_in_order(tid * kPer + j);
+    if (key_of(value_at(p)) <= edge || vs.w[p] < (double)min_p) vs.w[p] = 0.0;
+  }
+  const uint32_t edge_place = edge ? place_of(__float_as_uint(value_of(edge)) >> 16) : kValues + 1;
+  __syncthreads();
+  kept = 0.0;
+  ties = 0;
+  for (int vi = s0 + lane; vi < s1; vi += 32) {
+    if (vi >= row.full0 && vi < row.full1) {
+      const uint4 r = row.raw(vi);
+      const uint32_t word[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t bits = j & 1 ? word[j / 2] >> 16 : word[j / 2] & 0xFFFFu, p = place_of(bits);
+        if (p < kValues) {
+          kept += vs.w[p];
+          ties += p == edge_place;
+        } else {
+          const float x = fmaxf(__uint_as_float(bits << 16), -CUDART_INF_F);
+          if (x >= nothing && key_of(x) > edge) {
+            const double w = weight(x);
+            if (w >= (double)min_p) kept += w;
+          } else if (edge_place == kValues) {
+            ties += key_of(x) == edge;
+          }
+        }
+      }
+    } else {
+      float v[8];
+      row.load(vi, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t key = key_of(v[j]);
+        if (key > edge) {
+          const double w = weight(v[j]);
+          if (w >= (double)min_p) kept += w;
+        } else {
+          ties += key == edge;
+        }
+      }
+    }
+  }
+  return true;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   constexpr int N = Row<T>::N;
+  constexpr bool kByValues = sizeof(T) == 2;
   __shared__ SampleSmem sm;
+  extern __shared__ __align__(16) unsigned char smem_dyn[];
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Row<T> row(static_cast<const T *>(a.logits) + (long long)r * a.stride, a.V);
   const float u = a.uniform[r], t = a.temperature ? a.temperature[r] : 1.f;
@@ -542,7 +724,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   double kept_here = 0.0;             // kept weight above the border in this warp's segment
   int ties = 0;                       // equals of the border in it
   bool have_sums = false;
-  if (top_p < 1.f && !by_edge) {
+  if constexpr (kByValues) {
+    if (by_edge && top_p < 1.f) descend(row, weight, sm, true, top_k, top_p, edge, n_edge);
+    __syncthreads();
+    if (top < CUDART_INF_F)
+      have_sums = by_values(row, weight, sm, *reinterpret_cast<ValueSmem *>(smem_dyn), t, top_p, min_p,
+                            top_p < 1.f && !by_edge, edge, n_edge, s0, s1, kept_here, ties);
+    __syncthreads();
+    if (!have_sums && tid == 0) sm.n = 0;
+    __syncthreads();
+  }
+  if (have_sums) {
+  } else if (top_p < 1.f && !by_edge) {
     int listed = 0;                   // tokens of the list before the border
     const float scale = (float)(weight.c * (double)(kBins / kOctaves));
     const auto bin_of = [&](float x, float &z) {
@@ -770,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
       __syncthreads();
       descend(row, weight, sm, true, top_k, top_p, edge, n_edge);
     }
-  } else if (top_p < 1.f) {
+  } else if (top_p < 1.f && !kByValues) {
     descend(row, weight, sm, true, top_k, top_p, edge, n_edge);
   }
 
@@ -921,8 +1114,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &a, int in_dtype, cudaStream_t st) {
-  if (in_dtype == TV_F32) sample_kernel<float><<<a.R, kThreads, 0, st>>>(a);
-  else sample_kernel<__nv_bfloat16><<<a.R, kThreads, 0, st>>>(a);
+  if (in_dtype == TV_F32) {
+    sample_kernel<float><<<a.R, kThreads, 0, st>>>(a);
+  } else {
+    auto kernel = sample_kernel<__nv_bfloat16>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ValueSmem));
+    if (e != cudaSuccess) return e;
+    kernel<<<a.R, kThreads, sizeof(ValueSmem), st>>>(a);
+  }
   return cudaGetLastError();
 }
 

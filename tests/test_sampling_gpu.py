@@ -89,6 +89,22 @@ def test_ties():
     compare(z, [0.0, 0.5, 1.0, 0.5, 0.0, 0.999], top_k=np.int32([501, 7, 1, 999, 1000, 2000]))
 
 
+@pytest.mark.parametrize("scale,shift", [(0.01, 0.0), (1.0, 0.0), (6.0, 3.0), (1e-3, 0.0), (80.0, 0.0),
+                                         (3.0, 300.0), (3.0, -300.0), (1.0, 0.004)])
+def test_bf16_magnitudes(scale, shift):
+    """bf16 logits of magnitudes with and without a place of their own, zeros among them."""
+    R, V = 48, 6000
+    x = (logits(R, V, 30, scale=scale) + shift).to(BF16)
+    x[::2, ::7] = 0.0
+    x[1::4, ::5] = -math.inf
+    u = np.random.default_rng(31).random(R)
+    compare(x, u, **mixed(R, 32))
+    compare(x, u, top_p=np.linspace(0.02, 0.9999, R).astype(np.float32))
+    compare(x, u, min_p=np.linspace(0.0, 0.5, R).astype(np.float32))
+    compare(x.float(), u, top_p=np.linspace(0.02, 0.9999, R).astype(np.float32))
+    compare(x, u, top_k=np.full(R, 2000, np.int32), top_p=np.full(R, 0.7, np.float32))
+
+
 def test_ends_of_the_parameters():
     R, V = 12, 333
     x = logits(R, V, 14)
