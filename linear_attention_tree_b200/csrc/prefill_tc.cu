@@ -263,11 +263,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_wait_st();
         sy.arrive_tmem(kS0 + g);
       }
-      if (c > 0) {
+      // o of the chunk before: gated, while R T^T is computed; scalar decay, now, which frees what the
+      // operands are written over (storing it after them: 111 us for 8 x 1000 tokens against 90)
+      const auto write_last = [&] {
+        if (c == 0) return;
         ok = ok && sy.wait(kO0 + ((c - 1) & 1), (c - 1) >> 1);
         ptx::tc_fence_after();
         write_out(c - 1, ok);
-      }
+      };
+      if (!kGdn) write_last();
       ok = ok && sy.wait(kGates0 + (c & 3), c >> 2);
       // V (scalar decay: U = V at once)
       float u[16], gate[16];
@@ -295,12 +299,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tmem_wait_st();
         sy.arrive_tmem(kR);
+        write_last();
         gates(gt.tail, gate);
         ok = ok && sy.wait(kTR, c);
         ptx::tc_fence_after();
         tmem_load(tl + kColSK + 16 * part, u);
       } else {
-        // (the operands of the chunk before have been read: its o has been written)
         gates(gt.tail, gate);
       }
       // pieces of U~ (decayed to the chunk's end), one after the other, and U for the output
