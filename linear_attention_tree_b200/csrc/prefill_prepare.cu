@@ -5,14 +5,18 @@
 // into the workspace, for prefill_tc.cu, which carries the states from chunk to chunk.
 //
 // Persistent CTAs, three per SM, go through (chunk, head) items: warp 8 finds an item's sequence, brings
-// its q and k by TMA and makes its gates, an item ahead; warps 0-7 compute.  (A CTA per item took twice
-// as long: its loads in a row are 8 us, and four resident CTAs do not hide them.)  [Q;K] K^T is one
-// tcgen05 product (128 x 64) into tensor memory; a lane there is a row of P or of L.  T comes by the
-// 16 x 16 diagonal blocks, by substitution in fp32, one warp each, then the blocks below them by
-// products of 16 x 16 blocks: too small for tcgen05 (128 rows) and, as multiply-adds, bound by the
-// registers' fill from shared memory (128 bytes a cycle), so they are warp-level tf32 products of
-// high and low halves, a sixth of those reads.
-// The kernel runs apart from the chain over chunks, which it slowed by half when both shared an SM.
+// its q and k by TMA and makes its gates, an item ahead; warps 0-7 compute.  (Without that an item's
+// loads in a row are 8 us: 8 x 1000 tokens of scalar decay took 98 us in all with a CTA per item, 90 us
+// so.)  [Q;K] K^T is one tcgen05 product (128 x 64) into tensor memory; a lane there is a row of P or
+// of L.  T comes by the 16 x 16 diagonal blocks, by substitution in fp32, one warp each, then the
+// blocks below them by products of 16 x 16 blocks: too small for tcgen05 (128 rows) and, as
+// multiply-adds, bound by the registers' fill from shared memory (128 bytes a cycle), so they are
+// warp-level tf32 products of high and low halves (all shared-memory reads of the kernel halved, 67 to
+// 57 us for 2560 items).
+// The kernel runs apart from the chain over chunks, whose SMs it kept busy when both were one: 1 x 8192
+// tokens of 32 heads took 963 us then, 733 us as two kernels.
+// 4096 items (those 8192 tokens) take 72 us: 187 MB at 2.6 TB/s, the shared-memory pipe 76% busy, which
+// bounds it, issue slots 45%.
 //
 // Every wait is bounded: one that runs out records TV_ERR_TIMEOUT and ends the CTA.
 #include <algorithm>
