@@ -263,8 +263,8 @@ TV_API tv_status tv_snapshot_commit(const tv_problem *p, const float *snapshots,
  * model's logits,  tv_sample (one target token per node),  tv_tree_accept  and
  * tv_tree_commit;  tv_decode_step  takes the place of a tree for sequences without a draft.
  * The conventions above hold.  The recurrence is fp32 throughout: the states that these
- * entry points write are within a few 1e-7 of the exact ones (relative, 2-norm), and out is
- * rounded once to its type.  For a decay below exp(-1000) the result is that of a decay of
+ * entry points write are within 1e-6 of the exact ones (relative, 2-norm), and out is rounded
+ * once to its type.  For a decay below exp(-1000) the result is that of a decay of
  * zero, so log_a = -inf starts a state afresh. */
 
 /* The recurrence over whole prompts: for every token t of a sequence, in order,
@@ -279,7 +279,7 @@ TV_API tv_status tv_snapshot_commit(const tv_problem *p, const float *snapshots,
  *              last may end before T: rows that no sequence owns are neither read nor written.
  *              An empty sequence keeps its state                       (device, read)
  *   S_in       [B][H][dv][dk] fp32, or NULL for zero states             (device, read)
- *   out        [T][H][dv] out_dtype                                     (device, written)
+ *   out        [T][H][dv] out_dtype; must not overlap any input         (device, written)
  *   S_out      [B][H][dv][dk] fp32; may be S_in itself, must not partially overlap it
  *                                                                       (device, written)
  *   workspace  tv_prefill_workspace_size(p) bytes, as for trees: the status word alone, or, for

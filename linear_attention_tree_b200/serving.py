@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 
 import torch
 
@@ -131,24 +132,27 @@ def _workspace(t, problem, device):
 
 
 def _on_stream(f):
-    """Calls f with the call's stream handle as ``raw``.  Where ``stream`` or the device of the
+    """Calls f with the call's stream handle as ``_raw``.  Where ``stream`` or the device of the
     first argument is not the current one, they are made current, so that what f allocates
     belongs to the stream."""
+    name = next(iter(inspect.signature(f).parameters))
+
     @functools.wraps(f)
-    def call(first, *args, stream=None, **kwargs):
+    def call(*args, stream=None, **kwargs):
+        first = args[0] if args else kwargs.get(name)
         if not isinstance(first, torch.Tensor):
-            raise TypeError("the first argument must be a torch.Tensor")
+            raise TypeError(f"{name} must be a torch.Tensor")
         index = first.get_device()
         if index < 0:
-            raise ValueError("the arguments must live on a CUDA device")
+            raise ValueError(f"{name} must live on a CUDA device")
         if stream is None and index == torch.cuda.current_device():
-            return f(first, *args, raw=_raw_stream(index), **kwargs)
+            return f(*args, _raw=_raw_stream(index), **kwargs)
         if stream is None:
             stream = torch.cuda.current_stream(index)
         elif stream.device.index != index:
             raise ValueError("the stream belongs to another device than the arguments")
         with torch.cuda.stream(stream):
-            return f(first, *args, raw=stream.cuda_stream, **kwargs)
+            return f(*args, _raw=stream.cuda_stream, **kwargs)
     return call
 
 
@@ -170,7 +174,7 @@ def _sequence_call(q, v, mode, out, out_dtype):
 @_on_stream
 def prefill(q, k, v, log_a, b, seq_offsets, S_in=None, *, max_len: int, mode: str = "gdn",
             out=None, S_out=None, out_dtype=None, workspace=None, kernel: str = "auto",
-            raw=None):
+            _raw=None):
     """The recurrence over whole prompts; returns (out [T][H][dv], S_out [B][H][dv][dk] fp32).
 
     q, k [T][Hk][dk]; v [T][H][dv] (fp32 or bf16); log_a, b [T][H] fp32 (b may be None in
@@ -183,7 +187,7 @@ def prefill(q, k, v, log_a, b, seq_offsets, S_in=None, *, max_len: int, mode: st
     B = _dims(seq_offsets, "seq_offsets", 1)[0] - 1
     dev, dt = q.device, q.dtype
     at = dev.index
-    prob = _sequence_problem(B, H, dk, dv, T, max_len, 1, MODE[mode], DTYPE[dt], DTYPE[odt],
+    prob = _sequence_problem(B, H, dk, dv, T, int(max_len), 1, MODE[mode], DTYPE[dt], DTYPE[odt],
                              KERNEL[kernel], 0, Hk)
     if out is None:
         out = torch.empty((T, H, dv), dtype=odt, device=dev)
@@ -195,7 +199,7 @@ def prefill(q, k, v, log_a, b, seq_offsets, S_in=None, *, max_len: int, mode: st
         _arr(v, "v", dt, (T, H, dv), at), _arr(log_a, "log_a", _F32, (T, H), at),
         _arr(b, "b", _F32, (T, H), at), _arr(seq_offsets, "seq_offsets", _I32, (B + 1,), at),
         _arr(S_in, "S_in", _F32, (B, H, dv, dk), at), _arr(out, "out", odt, (T, H, dv), at),
-        _arr(S_out, "S_out", _F32, (B, H, dv, dk), at), ws, ws_bytes, raw)
+        _arr(S_out, "S_out", _F32, (B, H, dv, dk), at), ws, ws_bytes, _raw)
     if st:
         raise TreeVerifyError(st, "tv_prefill")
     return out, S_out
@@ -203,7 +207,7 @@ def prefill(q, k, v, log_a, b, seq_offsets, S_in=None, *, max_len: int, mode: st
 
 @_on_stream
 def decode_step(q, k, v, log_a, b, S, *, mode: str = "gdn", out=None, S_new=None, out_dtype=None,
-                raw=None):
+                _raw=None):
     """The recurrence for one token of every sequence; returns (out [B][H][dv], S_new).
 
     q, k [B][Hk][dk]; v [B][H][dv] (fp32 or bf16); log_a, b [B][H] fp32 (b may be None in
@@ -223,7 +227,7 @@ def decode_step(q, k, v, log_a, b, S, *, mode: str = "gdn", out=None, S_new=None
         prob, _arr(q, "q", dt, (B, Hk, dk), at), _arr(k, "k", dt, (B, Hk, dk), at),
         _arr(v, "v", dt, (B, H, dv), at), _arr(log_a, "log_a", _F32, (B, H), at),
         _arr(b, "b", _F32, (B, H), at), _arr(S, "S", _F32, (B, H, dv, dk), at),
-        _arr(out, "out", odt, (B, H, dv), at), _arr(S_new, "S_new", _F32, (B, H, dv, dk), at), raw)
+        _arr(out, "out", odt, (B, H, dv), at), _arr(S_new, "S_new", _F32, (B, H, dv, dk), at), _raw)
     if st:
         raise TreeVerifyError(st, "tv_decode_step")
     return out, S_new
@@ -231,7 +235,7 @@ def decode_step(q, k, v, log_a, b, S, *, mode: str = "gdn", out=None, S_new=None
 
 @_on_stream
 def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=None, token=None,
-           logprob=None, workspace=None, raw=None):
+           logprob=None, workspace=None, _raw=None):
     """One token per row of logits; returns (token [R] int32, logprob [R] fp32).
 
     logits [R][V] (fp32 or bf16; rows may be strided, values of a row adjacent); uniform [R]
@@ -259,7 +263,7 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
         _arr(temperature, "temperature", _F32, (R,), at), _arr(top_k, "top_k", _I32, (R,), at),
         _arr(top_p, "top_p", _F32, (R,), at), _arr(min_p, "min_p", _F32, (R,), at),
         _arr(token, "token", _I32, (R,), at), _arr(logprob, "logprob", _F32, (R,), at),
-        ws, ws_bytes, raw)
+        ws, ws_bytes, _raw)
     if st:
         raise TreeVerifyError(st, "tv_sample")
     return token, logprob
@@ -273,7 +277,7 @@ def _tree_problem(B, T, max_nodes, max_path) -> Problem:
 @_on_stream
 def tree_accept(draft_token, target_token, root_token, parent, node_offsets, *, max_nodes: int,
                 max_path: int, accepted_path=None, accepted_len=None, next_token=None,
-                workspace=None, raw=None):
+                workspace=None, _raw=None):
     """The accepted path of every draft tree; returns (accepted_path [B][max_path],
     accepted_len [B], next_token [B]), all int32, the first as `tree_commit` takes it.
 
@@ -286,7 +290,9 @@ def tree_accept(draft_token, target_token, root_token, parent, node_offsets, *, 
     B = _dims(node_offsets, "node_offsets", 1)[0] - 1
     dev = draft_token.device
     at = dev.index
-    prob = _tree_problem(B, T, max_nodes, max_path)
+    prob = _tree_problem(B, T, int(max_nodes), int(max_path))
+    if not isinstance(root_token, torch.Tensor):
+        raise TypeError("root_token must be a torch.Tensor")
     if root_token.dtype is not _I32:
         raise TypeError(f"root_token has dtype {root_token.dtype}, expected {_I32}")
     if accepted_path is None:
@@ -304,7 +310,7 @@ def tree_accept(draft_token, target_token, root_token, parent, node_offsets, *, 
         _arr(node_offsets, "node_offsets", _I32, (B + 1,), at),
         _arr(accepted_path, "accepted_path", _I32, (B, max_path), at),
         _arr(accepted_len, "accepted_len", _I32, seqs, at),
-        _arr(next_token, "next_token", _I32, seqs, at), ws, ws_bytes, raw)
+        _arr(next_token, "next_token", _I32, seqs, at), ws, ws_bytes, _raw)
     if st:
         raise TreeVerifyError(st, "tv_tree_accept")
     return accepted_path, accepted_len, next_token

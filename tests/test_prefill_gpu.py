@@ -383,6 +383,17 @@ def test_decode_step_resets_and_streams():
     assert torch.equal(o, o2) and torch.equal(S, S2)
 
 
+def test_keyword_calls():
+    d = inputs([5, 4], 2, 128, 128, seed=53)
+    kw = {n: d[n] for n in ("q", "k", "v", "log_a", "b")}
+    a = L.prefill(*kw.values(), d["offsets"], d["S"], max_len=5)
+    b = L.prefill(seq_offsets=d["offsets"], S_in=d["S"], max_len=np.int64(5), **kw)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    one = {n: x[:2].contiguous() for n, x in kw.items()}
+    a, b = L.decode_step(*one.values(), d["S"]), L.decode_step(S=d["S"], **one)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_refusals_by_the_binding():
     d = inputs([4], 2, 128, 128, seed=1)
     args = [d["q"], d["k"], d["v"], d["log_a"], d["b"], d["offsets"], d["S"]]
