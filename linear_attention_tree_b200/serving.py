@@ -190,7 +190,7 @@ def prefill(q, k, v, log_a, b, seq_offsets, S_in=None, *, max_len: int, mode: st
     prob = _sequence_problem(B, H, dk, dv, T, int(max_len), 1, MODE[mode], DTYPE[dt], DTYPE[odt],
                              KERNEL[kernel], 0, Hk)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=odt, device=dev)
+        out = torch.empty_like(v) if odt is v.dtype else torch.empty_like(v, dtype=odt)
     if S_out is None:
         S_out = torch.empty((B, H, dv, dk), dtype=_F32, device=dev)
     ws, ws_bytes, _kept = _workspace(workspace, prob, dev)
@@ -219,8 +219,7 @@ def decode_step(q, k, v, log_a, b, S, *, mode: str = "gdn", out=None, S_new=None
     at = dev.index
     prob = _sequence_problem(B, H, dk, dv, B, 1, 1, MODE[mode], DTYPE[dt], DTYPE[odt], 0, 0, Hk)
     if out is None:
-        out = v.new_empty((B, H, dv)) if odt is v.dtype else \
-            torch.empty((B, H, dv), dtype=odt, device=dev)
+        out = torch.empty_like(v) if odt is v.dtype else torch.empty_like(v, dtype=odt)
     if S_new is None:
         S_new = torch.empty((B, H, dv, dk), dtype=_F32, device=dev)
     st = _library().tv_decode_step(
@@ -254,9 +253,9 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
     prob = SampleProblem(R, V, logits.stride(0) if R > 1 else V, DTYPE[logits.dtype], 0)
     uniform_at = _arr(uniform, "uniform", _F32, (R,), at)
     if token is None:
-        token = torch.empty(R, dtype=_I32, device=dev)
+        token = torch.empty_like(uniform, dtype=_I32)
     if logprob is None:
-        logprob = uniform.new_empty(R)
+        logprob = torch.empty_like(uniform)
     ws, ws_bytes, _kept = _workspace(workspace, prob, dev)
     st = _library().tv_sample(
         prob, logits.data_ptr(), uniform_at,
@@ -298,9 +297,9 @@ def tree_accept(draft_token, target_token, root_token, parent, node_offsets, *, 
     if accepted_path is None:
         accepted_path = root_token.new_empty((B, max_path))
     if accepted_len is None:
-        accepted_len = root_token.new_empty(B)
+        accepted_len = torch.empty_like(root_token)
     if next_token is None:
-        next_token = root_token.new_empty(B)
+        next_token = torch.empty_like(root_token)
     ws, ws_bytes, _kept = _workspace(workspace, prob, dev)
     nodes, seqs = (T,), (B,)
     st = _library().tv_tree_accept(
