@@ -29,9 +29,9 @@
 //                  a value (4096 of them) and not for a logit, top-p's border is known from the
 //                  counts alone, and the sums by segments look weights up.  The few others go by
 //                  the exponential.
-// 2048 rows of 65536 bf16 logits with mixed filters take 214 us (268 MB; greedy alone 58 us, 4.6 TB/s;
-// top-k of 50 114 us, no filter 218 us, top-p 330 us), 128 rows of 100003 in fp32 112 us, one of 32768
-// 30 us: instructions and the barriers between a row's steps bound it, not bytes.
+// 2048 rows of 65536 bf16 logits with mixed filters take 205 us (268 MB; greedy alone 59 us, 4.6 TB/s;
+// top-k of 50 114 us, no filter 208 us, top-p 308 us), 128 rows of 100003 in fp32 103 us, one of 32768
+// with top-p 28 us: instructions and the barriers between a row's steps bound it, not bytes.
 // The segment that holds the token is then read once more.  Where a list overflows or top-k is
 // large, the border comes from a radix descent over the logits' bits (slow and general).
 // Second and later reads hit L2.
@@ -83,7 +83,6 @@ struct SampleSmem {
   int n, pick, ties_left, around[2];
   uint32_t digit;
   u64 before;
-  double base, target, total;
 };
 
 // exp((x - m) / t) in 64 bits, as 2^(i/16 + r): a table of 2^(j/16), whose 16 entries lie in
@@ -171,7 +170,19 @@ template <> __device__ __forceinline__ void Row<__nv_bfloat16>::widen(uint4 r, f
   }
 }
 
-// Sums over the block in a fixed order; every thread gets the result.
+// Inclusive prefix over the warp.
+template <typename U> __device__ __forceinline__ U warp_scan(U v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const U y = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// Sums over the block in a fixed order; every thread gets the result.  (Each warp goes through the
+// warps' parts by shuffles: five steps where adding them up in a row takes 32.)
 template <int kThreads>
 __device__ __forceinline__ double block_sum(double v, double *part) {
   constexpr int kWarps = kThreads / 32;
@@ -180,9 +191,9 @@ __device__ __forceinline__ double block_sum(double v, double *part) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = part[0];
+  v = (threadIdx.x & 31) < kWarps ? part[threadIdx.x & 31] : 0.0;
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) v += part[w];
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
 
@@ -192,39 +203,22 @@ __device__ __forceinline__ void block_scan(double v, int c, SampleSmem &sm, doub
                                            int &c_before, double &v_all, int &c_all) {
   constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double s = v;
-  int k = c;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(kFull, s, o);
-    const int z = __shfl_up_sync(kFull, k, o);
-    if (lane >= o) {
-      s += y;
-      k += z;
-    }
-  }
+  const double s = warp_scan(v);
+  const int k = warp_scan(c);
   __syncthreads();
   if (lane == 31) {
     sm.part[warp] = s;
     sm.ipart[warp] = k;
   }
   __syncthreads();
-  double b = 0.0;
-  int kb = 0;
-  v_all = 0.0;
-  c_all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) {
-      b = v_all;
-      kb = c_all;
-    }
-    v_all += sm.part[w];
-    c_all += sm.ipart[w];
-  }
-  const double up = __shfl_up_sync(kFull, s, 1);
-  v_before = b + (lane ? up : 0.0);
-  c_before = kb + k - c;
+  const double parts = warp_scan(lane < kWarps ? sm.part[lane] : 0.0);
+  const int iparts = warp_scan(lane < kWarps ? sm.ipart[lane] : 0);
+  v_all = __shfl_sync(kFull, parts, 31);
+  c_all = __shfl_sync(kFull, iparts, 31);
+  const double b = __shfl_sync(kFull, parts, max(warp - 1, 0)), up = __shfl_up_sync(kFull, s, 1);
+  const int kb = __shfl_sync(kFull, iparts, max(warp - 1, 0));
+  v_before = (warp ? b : 0.0) + (lane ? up : 0.0);
+  c_before = (warp ? kb : 0) + k - c;
 }
 
 // sorted = list[0..n) in falling order, by counting what is larger (the entries differ).
@@ -1023,39 +1017,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     sm.ipart[warp] = ties;
   }
   __syncthreads();
-  if (tid == 0) {
-    double total = 0.0;
-    int left = n_edge;
-    for (int w = 0; w < kWarps; ++w) {
-      const int k = min(left, sm.ipart[w]);
-      total += sm.part[w] + k * w_edge;
-      left -= k;
-    }
-    const double target = (double)u * total;
-    double c = 0.0;
-    left = n_edge;
-    for (int w = 0; w < kWarps; ++w) {
-      const int k = min(left, sm.ipart[w]);
-      const double m = sm.part[w] + k * w_edge;
-      if (m > 0.0) {                  // the last segment with weight, or the first past the target
-        sm.pick = w;
-        sm.ties_left = left;
-        sm.base = c;
-        if (c + m > target) break;
-      }
-      c += m;
-      left -= k;
-    }
-    sm.total = total;
-    sm.target = target;
-  }
-  __syncthreads();
+  // every warp by itself: lane w has segment w.  The first segment past the target, or the last with
+  // weight
+  const int equals = lane < kWarps ? sm.ipart[lane] : 0, equals_before = warp_scan(equals) - equals;
+  const double in_segment =
+      lane < kWarps ? sm.part[lane] + min(max(n_edge - equals_before, 0), equals) * w_edge : 0.0;
+  const double end = warp_scan(in_segment), total = __shfl_sync(kFull, end, 31), target = (double)u * total;
+  const unsigned weighs = __ballot_sync(kFull, in_segment > 0.0);
+  const unsigned beyond = __ballot_sync(kFull, in_segment > 0.0 && end > target);
+  const int pick = beyond ? __ffs(beyond) - 1 : weighs ? 31 - __clz(weighs) : 0;
+  const double start = __shfl_sync(kFull, end, max(pick - 1, 0));
+  double base = pick ? start : 0.0;
+  int left = max(n_edge - __shfl_sync(kFull, equals_before, pick), 0);
 
   // ---- the token: the whole block over its segment --------------------------------------------
-  const int e0 = min(row.vectors, sm.pick * seg), e1 = min(row.vectors, e0 + seg);
-  const double target = sm.target, total = sm.total;
-  double base = sm.base;
-  int left = sm.ties_left;
+  const int e0 = min(row.vectors, pick * seg), e1 = min(row.vectors, e0 + seg);
   for (int v0 = e0; v0 < e1; v0 += kThreads) {
     const int vi = v0 + tid;
     float v[N];
