@@ -30,8 +30,8 @@
 //                  counts alone, and the sums by segments look weights up.  The few others go by
 //                  the exponential.
 // 2048 rows of 65536 bf16 logits with mixed filters take 205 us (268 MB; greedy alone 59 us, 4.6 TB/s;
-// top-k of 50 114 us, no filter 208 us, top-p 308 us), 128 rows of 100003 in fp32 103 us, one of 32768
-// with top-p 28 us: instructions and the barriers between a row's steps bound it, not bytes.
+// top-k of 50 114 us, no filter 208 us, top-p 308 us), 128 rows of 100003 in fp32 105 us, one of 32768
+// with top-p 25 to 50 us by temperature and top_p: instructions and the barriers between a row's steps bound it, not bytes.
 // The segment that holds the token is then read once more.  Where a list overflows or top-k is
 // large, the border comes from a radix descent over the logits' bits (slow and general).
 // Second and later reads hit L2.
@@ -1101,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
 }
 
 // Rows that leave SMs free have 1024 threads each, two of 512 share an SM otherwise: 128 rows of 100003
-// logits in fp32, all filters, take 92 us with 1024 threads and 140 us with 512; 1024 rows of 50000
+// logits in fp32 with mixed filters took 112 us with 1024 threads and 140 us with 512; 1024 rows of 50000
 // 214 and 193 us.
 template <typename T, int kThreads> cudaError_t launch_rows(const SampleArgs &a, cudaStream_t st) {
   constexpr int kBytes = sizeof(T) == 2 ? (int)sizeof(ValueSmem) : 0;

@@ -37,7 +37,7 @@ def compare(x, u, **p):
     lp = lp.cpu().numpy().astype(np.float64)
     fin = np.isfinite(wlp)
     assert np.array_equal(fin, np.isfinite(lp)) and np.all(lp[~fin] == -np.inf)
-    assert np.all(np.abs(lp - wlp)[fin] <= 2.0 ** -24 * np.abs(wlp[fin]) + 2.0 ** -40)
+    assert np.all(np.abs(lp[fin] - wlp[fin]) <= 2.0 ** -24 * np.abs(wlp[fin]) + 2.0 ** -40)
     return got
 
 
