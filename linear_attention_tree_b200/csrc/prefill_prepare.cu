@@ -146,21 +146,24 @@ __device__ __forceinline__ void invert(Matrices &m, int w, int lane) {
   }
   group_sync(1, kWarps * 32);
   const int c0 = 8 * (w & 1);                     // eight columns of a block to a warp
+  float pair[4] = {};                             // T_10 or T_32
   if (w < 4) {
     const int b = w >> 1, J = 2 * b, i = J + 1;
-    float acc[4] = {}, out[4] = {};
+    float acc[4] = {};
     block_product(acc, &m.L[16 * i][16 * J], &m.Tt[16 * J + c0][16 * J], kLd, lane);
     store_columns(y_at(m, b, c0), kLd, acc, 1.f, lane);
     __syncwarp();
-    block_product(out, &m.L[16 * i][16 * i], y_at(m, b, c0), kLd, lane);
-    store_columns(&m.Tt[16 * J + c0][16 * i], kLd, out, -1.f, lane);
-    if (b == 1) {                                 // T_32 by rows too, over L_32
-      const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m.L[48 + g + 8 * (e >> 1)][32 + c0 + 2 * t + (e & 1)] = -out[e];
-    }
+    block_product(pair, &m.L[16 * i][16 * i], y_at(m, b, c0), kLd, lane);
+    store_columns(&m.Tt[16 * J + c0][16 * i], kLd, pair, -1.f, lane);
   }
   group_sync(1, kWarps * 32);
+  if (w == 2 || w == 3) {
+    // T_32 by rows too, over L_32, which both of these warps read whole before the barrier; it is read
+    // in the last step
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m.L[48 + g + 8 * (e >> 1)][32 + c0 + 2 * t + (e & 1)] = -pair[e];
+  }
   const int I = 2 + (w >> 2), J = w >> 1 & 1;
   {
     float acc[4] = {};

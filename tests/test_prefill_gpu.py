@@ -145,6 +145,26 @@ def test_rows_of_others_may_hold_anything(kernel, mode):
             check(o[off[s]:off[s + 1]], want[0][off[s]:off[s + 1]], tol(100, odt), "out")
 
 
+@pytest.mark.parametrize("mode", ["gdn"])
+@pytest.mark.parametrize("n", [64])
+def test_equal_prompts_give_equal_bits(mode, n):
+    """Thousands of chunks of the same tokens: every one has the first one's bits, whichever warp
+    of its CTA comes first at each step."""
+    B, H = 1200, 4
+    d = inputs([n], H, 128, 128, seed=59, mode=mode, zero=True)
+    want = recurrence(d, [n], mode)
+    d["offsets"] = torch.arange(0, (B + 1) * n, n, dtype=torch.int32, device="cuda")
+    for name in ("q", "k", "v", "log_a", "b"):
+        if d[name] is not None:
+            d[name] = d[name].repeat((B,) + (1,) * (d[name].dim() - 1))
+    for _ in range(3):
+        o, S = run_prefill(d, [n] * B, mode, "tc", F32)
+        o = o.view(B, n, H, 128)
+        assert (o == o[0]).all() and (S == S[0]).all()
+        check(o[0], want[0], tol(n, F32), "out")
+        check(S[:1], want[1], tol(n), "state")
+
+
 @pytest.mark.parametrize("kernel", ["tc", "simt"])
 def test_many_ragged_sequences(kernel):
     g = np.random.default_rng(5)
