@@ -378,6 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // blocks above the diagonal stay zero
     for (int e = pt; e < (4 * kTAtom + 2 * kPBytes) / 16; e += kPrep * 32)
       *reinterpret_cast<uint4 *>(sm + kOffT + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+    // what one of these warps zeroes, another may write: none starts before all are through
+    group_sync(2, kPrep * 32);
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
       unsigned char *tile = sm + (c & 1) * kTileBytes;

@@ -145,8 +145,8 @@ def test_rows_of_others_may_hold_anything(kernel, mode):
             check(o[off[s]:off[s + 1]], want[0][off[s]:off[s + 1]], tol(100, odt), "out")
 
 
-@pytest.mark.parametrize("mode", ["gdn"])
-@pytest.mark.parametrize("n", [64])
+@pytest.mark.parametrize("mode", ["gdn", "scalar"])
+@pytest.mark.parametrize("n", [64, 130])
 def test_equal_prompts_give_equal_bits(mode, n):
     """Thousands of chunks of the same tokens: every one has the first one's bits, whichever warp
     of its CTA comes first at each step."""
