@@ -10,12 +10,12 @@
 //     S' = g S + sum_i exp(cl_last - cl_i) u_i k_i^T          (scalar decay: U = V).
 // Everything is kept transposed as in the verify kernels: tensor-memory lane = value row v.
 //
-// Precision.  States are fp32 and every product on their path is as good: a bf16 operand (k, q)
-// meets an fp32 one cut into three bf16 pieces of 8 bits (exact), T and R meet as pairs of tf32
-// (22 bits; the product of the two low parts, 2^-22 and less, is left out).  The output's own
-// products are as good where out is fp32.  Where it is bf16 (2^-8), S Q^T takes two pieces of S
-// (16 bits) and U P^T is one tf32 product (11 bits).  Decay ratios are powers of two of a
-// difference of sums kept as an fp32 pair.
+// Precision.  States are fp32 and every product is as good: a bf16 operand (k, q) meets an fp32 one cut
+// into three bf16 pieces of 8 bits (exact), T and R meet as pairs of tf32 (22 bits; the product of the
+// two low parts, 2^-22 and less, is left out), U and P as three bf16 pieces each (products of 2^-24
+// and less are left out).  out in bf16 is out in fp32 rounded once: with two pieces of S for S Q^T and one tf32
+// product U P^T for it, 3% of its values were a step off and the three times below 5 to 6% shorter.
+// Decay ratios are powers of two of a difference of sums kept as an fp32 pair.
 //
 // P and T of every chunk come from prefill_prepare.cu through the workspace; the states' chain runs
 // here, one CTA of 22 warps per (sequence, head), one per SM.  The chain of a chunk is
@@ -32,13 +32,15 @@
 // Rows of a last partial chunk past the sequence are zeroed in shared memory (k and v), so that
 // they add nothing.
 //
-// What bounds it is the chain: 7,600 cycles a chunk (4.1 us), of which the three products on it are
-// 2,650 back to back (24 + 24 MMAs of 37 cycles, 12 of 74) and the rest the chain warps' own work on
-// 128 x 128 values of S and 128 x 64 of R and U at half of the issue slots.  One prompt of 8192 tokens,
-// 32 heads, has 32 chains of 128 chunks: 560 us here, 72 us in prefill_prepare.cu (floor of the bytes:
-// 41 us).  16 ragged prompts of 16384 tokens in all: 467 us with it (floor 72 us), 8 x 1000 tokens of
-// scalar decay, 16 heads: 89 us (floor 23 us).  Sixteen chain warps instead of eight (latency), U~ and
-// S handed over piece by piece and o stored while R T^T is computed took the chain from 9,300 to 7,600.
+// What bounds it is the chain: 8,100 cycles a chunk (4.6 us), of which the three products on it are
+// 2,650 back to back (24 + 24 MMAs of 37 cycles, 12 of 74); the rest is the chain warps' own work on
+// 128 x 128 values of S and 128 x 64 of R and U at half of the issue slots, and the output's products.
+// One prompt of 8192 tokens, 32 heads, has 32 chains of 128 chunks: 595 us here, 72 us in
+// prefill_prepare.cu (floor of the bytes: 41 us).  16 ragged prompts of 16384 tokens in all: 505 us with it
+// (floor 72 us), 8 x 1000 tokens of scalar decay, 16 heads: 95 us (floor 23 us).  Sixteen chain warps
+// instead of eight (latency), U~ and S handed over piece by piece and o stored while R T^T is computed
+// shortened a chunk by 1,700 cycles.  22 warps leave 80 registers a thread, of which the chain spills 20
+// to 25.
 //
 // Every wait is bounded: one that runs out records TV_ERR_TIMEOUT on the status word and ends the
 // CTA after its copies and MMAs (bounded again).
@@ -63,7 +65,7 @@ constexpr int kTileBytes = 2 * kHalf + kC * 256;      // q, k, v of a chunk: 48 
 constexpr int kOffV = 2 * kHalf;
 constexpr int kOffT = 2 * kTileBytes;        // T: high and low tf32, each two atoms of 32 columns
 constexpr int kTAtom = kC * 128;
-constexpr int kPPart = kC * 128;             // P, two buffers: three bf16 pieces, or two tf32 atoms
+constexpr int kPPart = kC * 128;             // P, two buffers of three bf16 pieces
 constexpr int kPBytes = 3 * kPPart;
 constexpr int kOffP = kOffT + 4 * kTAtom;
 constexpr int kOffStage = kOffP + 2 * kPBytes;          // the workspace's blocks, two buffers
@@ -141,7 +143,6 @@ template <bool kGdn, typename Tout>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, SequenceArgs a) {
-  constexpr int kNO = sizeof(Tout) == 2 ? 2 : 3;            // pieces in the output's products
   extern __shared__ unsigned char smem_dyn[];
   unsigned char *sm = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -331,18 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             sy.arrive_tmem(kU0 + p);
           }
         }
-        if (kNO == 3) {
-          uint32_t packed[8];
+        uint32_t packed[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) packed[i] = cut(u[2 * i], u[2 * i + 1]);
-          tmem_store8(tl + kColU + 8 * part, packed);
-          store_pieces<2>(tl + kColSK + 16 * part, 8, u);
-        } else {
-          // U in tf32, over the accumulator it came from
-#pragma unroll
-          for (int j = 0; j < 16; ++j) u[j] = tf32_round(u[j]);
-          ptx::tmem_st16(tl + kColSK + 16 * part, u);
-        }
+        for (int i = 0; i < 8; ++i) packed[i] = cut(u[2 * i], u[2 * i + 1]);
+        tmem_store8(tl + kColU + 8 * part, packed);
+        store_pieces<2>(tl + kColSK + 16 * part, 8, u);      // over the accumulator it came from
       }
       ptx::tmem_wait_st();
       sy.arrive_tmem(kU2);
@@ -405,18 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = e0 + pt, b = e >> 6, I = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3;
         const int row = 16 * I + (e >> 2 & 15), i4 = 4 * (b - I * (I + 1) / 2) + (e & 3);   // columns 4 i4
         const float4 x = blocks[e];
-        const int atom = i4 >> 3, at = row * 128 + (((i4 & 7) ^ (row & 7)) << 4);
-        if (kNO == 3) {
-          float y[4] = {x.x, x.y, x.z, x.w};
-          const int at2 = row * 128 + (((i4 >> 1) ^ (row & 7)) << 4) + (i4 & 1) * 8;
+        float y[4] = {x.x, x.y, x.z, x.w};
+        const int at = row * 128 + (((i4 >> 1) ^ (row & 7)) << 4) + (i4 & 1) * 8;
 #pragma unroll
-          for (int p = 0; p < 3; ++p) {
-            const uint32_t lo2 = cut(y[0], y[1]), hi2 = cut(y[2], y[3]);
-            *reinterpret_cast<uint2 *>(po + p * kPPart + at2) = make_uint2(lo2, hi2);
-          }
-        } else {
-          *reinterpret_cast<float4 *>(po + atom * kPPart + at) =
-              make_float4(tf32_round(x.x), tf32_round(x.y), tf32_round(x.z), tf32_round(x.w));
+        for (int p = 0; p < 3; ++p) {
+          const uint32_t lo2 = cut(y[0], y[1]), hi2 = cut(y[2], y[3]);
+          *reinterpret_cast<uint2 *>(po + p * kPPart + at) = make_uint2(lo2, hi2);
         }
         if (kGdn) {
           // T's blocks are transposed: four rows of column e / 4
@@ -576,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
-        for (int p = 0; p < kNO; ++p)
+        for (int p = 0; p < 3; ++p)
           mma_f16(one, tm + kColSQ, tm + kColS + 64 * p + 8 * kk, q + step(kHalf, kk), kId64, kk + p > 0);
       mma_done(one, sy.at(kSQ));
       // U~ K over the columns of S, which S Q^T must have read
@@ -595,23 +583,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_done(one, sy.at(kD));
       {
         const uint64_t pd = d_p + ((c & 1) * kPBytes >> 4);
-        if (kNO == 3) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            // piece p of U at its columns, piece r of P
+        for (int kk = 0; kk < 4; ++kk) {
+          // piece p of U at its columns, piece r of P
 #pragma unroll
-            for (int p = 0; p < 3; ++p) {
-              const uint32_t up =
-                  p == 0 ? kColU + 8 * kk : kColSK + 16 * kk + 8 * (p - 1);
+          for (int p = 0; p < 3; ++p) {
+            const uint32_t up = p == 0 ? kColU + 8 * kk : kColSK + 16 * kk + 8 * (p - 1);
 #pragma unroll
-              for (int r = 0; r < 3 - p; ++r)
-                mma_f16(one, tm + kColUP, tm + up, pd + ((r * kPPart + kk * 32) >> 4), kId64, kk + p + r > 0);
-            }
+            for (int r = 0; r < 3 - p; ++r)
+              mma_f16(one, tm + kColUP, tm + up, pd + ((r * kPPart + kk * 32) >> 4), kId64, kk + p + r > 0);
           }
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_tf32(one, tm + kColUP, tm + kColSK + 8 * kk, pd + step(kPPart, kk), kIdT, kk > 0);
         }
         mma_done(one, sy.at(kO0 + (c & 1)));
       }

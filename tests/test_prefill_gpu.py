@@ -361,6 +361,22 @@ def test_rows_past_32_bits():
     assert not out[:T - n].any()
 
 
+@pytest.mark.parametrize("kernel", ["tc", "simt", "decode"])
+@pytest.mark.parametrize("mode", ["gdn", "scalar"])
+def test_out_is_rounded_once(kernel, mode):
+    """out in bf16 is out in fp32 rounded, bit for bit: its products are no coarser."""
+    lens = [1] * 300 if kernel == "decode" else [300, 70, 1]
+    d = inputs(lens, 4, 128, 128, seed=67, Hk=2, mode=mode)
+
+    def run(odt):
+        if kernel == "decode":
+            return L.decode_step(d["q"], d["k"], d["v"], d["log_a"], d["b"], d["S"], mode=mode,
+                                 out_dtype=odt)
+        return run_prefill(d, lens, mode, kernel, odt)
+    (o16, S16), (o32, S32) = run(BF16), run(F32)
+    assert torch.equal(o16, o32.to(BF16)) and torch.equal(S16, S32)
+
+
 # ---- single tokens ---------------------------------------------------------------------------
 
 
