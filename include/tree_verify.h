@@ -264,8 +264,9 @@ TV_API tv_status tv_snapshot_commit(const tv_problem *p, const float *snapshots,
  * tv_tree_commit;  tv_decode_step  takes the place of a tree for sequences without a draft.
  * The conventions above hold.  The recurrence is fp32 throughout: the states that these
  * entry points write are within 1e-6 of the exact ones (relative, 2-norm), and out is rounded
- * once to its type.  For a decay below exp(-1000) the result is that of a decay of
- * zero, so log_a = -inf starts a state afresh. */
+ * once to its type.  A decay of zero (log_a = -inf, or so low that exp(log_a) is 0 in fp32)
+ * starts a state afresh: at the first token of a call whatever the state given holds, NaN and
+ * infinities too; at later tokens of a prompt, from a finite state. */
 
 /* The recurrence over whole prompts: for every token t of a sequence, in order,
  *   S_t as above from S_{t-1},  out_t = S_t q_t,

@@ -67,6 +67,12 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(SequenceArgs a) {
     }
   }
   const float decay = expf(a.log_a[item]), b = kGdn ? a.b[item] : 0.f;
+  if (decay == 0.f) {                  // starts afresh, also from NaN and infinity
+#pragma unroll
+    for (int r = 0; r < kRowsPerThread; ++r)
+#pragma unroll
+      for (int i = 0; i < NK; ++i) S[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
 
 #pragma unroll
   for (int r = 0; r < kRowsPerThread; ++r) {

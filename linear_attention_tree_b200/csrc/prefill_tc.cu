@@ -191,9 +191,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     float S[2][16];
     const size_t mine = state + (size_t)v * 128 + 32 * part;
+    // (a first decay of zero starts afresh, also from NaN and infinity, which the products would spread)
+    const bool from = a.S_in && expf(a.log_a[(size_t)lo * H + h]) != 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 x = a.S_in ? *reinterpret_cast<const float4 *>(a.S_in + mine + 4 * i)
+      const float4 x = from ? *reinterpret_cast<const float4 *>(a.S_in + mine + 4 * i)
                               : make_float4(0.f, 0.f, 0.f, 0.f);
       S[i >> 2][4 * (i & 3)] = x.x;
       S[i >> 2][4 * (i & 3) + 1] = x.y;

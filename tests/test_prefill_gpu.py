@@ -248,6 +248,32 @@ def test_reset(kernel, mode, value):
     compare(d, lens, mode, run_prefill(d, lens, mode, kernel=kernel, out_dtype=F32))
 
 
+@pytest.mark.parametrize("kernel", ["tc", "simt", "decode"])
+@pytest.mark.parametrize("mode", ["gdn", "scalar"])
+@pytest.mark.parametrize("value", [-math.inf, -200.0])
+@pytest.mark.parametrize("held", [math.nan, math.inf])
+def test_reset_of_a_recycled_state(kernel, mode, value, held):
+    """A first decay of zero starts afresh from a state that holds anything, in place too."""
+    lens = [1, 1, 1] if kernel == "decode" else [140, 3, 64]
+    d = inputs(lens, 2, 128, 128, seed=71, mode=mode)
+    d["log_a"][d["offsets"][:-1].long()] = value
+    d["S"][:2] = held
+    if kernel == "simt":                     # token by token, at any token
+        d["log_a"][[64, 100]] = value
+        d["v"][63] = held
+    # (a decay that is zero in fp32 is zero; in 64 bits e^-200 would keep the NaN)
+    zero = torch.where(d["log_a"].exp() == 0, -math.inf, d["log_a"])
+    want = recurrence(dict(d, log_a=zero), lens, mode)
+    if kernel == "decode":
+        got = L.decode_step(d["q"], d["k"], d["v"], d["log_a"], d["b"], d["S"], mode=mode,
+                            S_new=d["S"], out_dtype=F32)
+    else:
+        got = run_prefill(d, lens, mode, kernel, F32, S_out=d["S"])
+    check(got[1], want[1], tol(max(lens)), "state")
+    rows = [t for t in range(sum(lens)) if kernel != "simt" or t != 63]
+    check(got[0][rows], want[0][rows], tol(max(lens), F32), "out")
+
+
 @pytest.mark.parametrize("mode", ["gdn", "scalar"])
 def test_splitting_a_prompt(mode):
     """A prompt in two calls, the state carried (in place), is the prompt in one."""
