@@ -48,7 +48,7 @@ constexpr int kSmallK = 256;                   // largest top-k that goes by str
 constexpr int kBins = 2048;
 constexpr float kOctaves = 48.f;               // the bins' range: weights down to 2^-48
 constexpr float kPhase = 2048.f;               // steps of a token's place in its bin: a million fit 32 bits
-constexpr double kScale = 4398046511104.0;     // 2^42: a million weights stay below 2^62
+constexpr double kScale = 4398046511104.0;     // 2^42: a million weights stay below 2^62, twice over
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;   // key of -inf
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -73,16 +73,30 @@ struct SampleSmem {
   double table[16];                            // 2^(j/16)
   union {
     struct { unsigned count[kBins], phase[kBins]; } bin;
-    u64 hist[256];
+    struct { u64 sum[256], low[256]; } hist;
     struct { double w[kList], w_by_index[kList]; } list_w;
   };
   u64 list[kList], sorted[kList];
   double part[kMaxWarps];
   int ipart[kMaxWarps];
-  u64 upart[kMaxWarps];
+  u64 upart[kMaxWarps], upart_low[kMaxWarps];
   int n, pick, ties_left, around[2];
   uint32_t digit;
-  u64 before;
+  u64 before, before_low;
+};
+
+// A sum of weights (of at most 1) as two integers, in steps of 2^-42 and of 2^-84, whose order in the atomics
+// does not matter.  The second holds what the first leaves: the border of a top_p next to 1 lies among
+// weights of 2^-43, and a sum over a million tokens has to be known to a small part of one.
+struct Mass {
+  u64 sum, low;
+  static __device__ __forceinline__ Mass of(double w) {
+    const double x = w * kScale, whole = floor(x);
+    return {(u64)whole, (u64)__double2ll_rn((x - whole) * kScale)};
+  }
+  __device__ __forceinline__ void add(Mass o) { sum += o.sum; low += o.low; }
+  __device__ __forceinline__ bool any() const { return sum || low; }
+  __device__ __forceinline__ double value() const { return (double)sum + (double)low / kScale; }   // times 2^42
 };
 
 // exp((x - m) / t) in 64 bits, as 2^(i/16 + r): a table of 2^(j/16), whose 16 entries lie in
@@ -344,74 +358,83 @@ __device__ void filled_around(SampleSmem &sm, int &before, int &after) {
   after = sm.around[1] == kBins ? pick : sm.around[1];
 }
 
-// Border of top-k (by count) or of top-p (by mass) through the bits of the keys, eight at a
-// time: masses are 64-bit integers (weight * 2^42), whose order in the atomics does not matter.
+// Border of top-k (by count) or of top-p (by mass) through the bits of the keys, eight at a time.
 // General and slow: up to five reads of the row.
 template <int kThreads, typename T>
 __device__ void descend(const Row<T> &row, const Weigher &weight, SampleSmem &sm, bool by_mass,
                         int top_k, float top_p, uint32_t &edge, int &n_edge) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x;
-  const auto fixed = [](double w) { return (u64)__double2ll_rn(w * kScale); };
-  double goal = 0.0;
+  double goal = (double)top_k;
   if (by_mass) {
-    u64 mass = 0;
+    Mass mass = {0, 0};
     for (int i = tid; i < row.V; i += kThreads) {
       const float x = fmaxf(to_f32(row.x[i]), -CUDART_INF_F);
-      if (key_of(x) > edge) mass += fixed(weight(x));
+      if (key_of(x) > edge) mass.add(Mass::of(weight(x)));
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(kFull, mass, o);
+    for (int o = 16; o; o >>= 1)
+      mass.add({__shfl_xor_sync(kFull, mass.sum, o), __shfl_xor_sync(kFull, mass.low, o)});
     __syncthreads();
-    if ((tid & 31) == 0) sm.upart[tid >> 5] = mass;
+    if ((tid & 31) == 0) {
+      sm.upart[tid >> 5] = mass.sum;
+      sm.upart_low[tid >> 5] = mass.low;
+    }
     __syncthreads();
-    mass = edge ? n_edge * fixed(weight(value_of(edge))) : 0;
-    for (int w = 0; w < kWarps; ++w) mass += sm.upart[w];
-    goal = (double)top_p * (double)mass;
+    mass = edge ? Mass::of(weight(value_of(edge))) : Mass{0, 0};
+    mass.sum *= n_edge;
+    mass.low *= n_edge;
+    for (int w = 0; w < kWarps; ++w) mass.add({sm.upart[w], sm.upart_low[w]});
+    goal = (double)top_p * mass.value();
   }
   uint32_t prefix = 0, mask = 0;
-  u64 before = 0;
+  Mass before = {0, 0};
   for (int shift = 24; shift >= 0; shift -= 8) {
     __syncthreads();
-    if (tid < 256) sm.hist[tid] = 0;
+    if (tid < 256) sm.hist.sum[tid] = sm.hist.low[tid] = 0;
     __syncthreads();
     for (int i = tid; i < row.V; i += kThreads) {
       const float x = fmaxf(to_f32(row.x[i]), -CUDART_INF_F);
       const uint32_t key = key_of(x);
-      if (key >= edge && (key & mask) == prefix)
-        atomicAdd(&sm.hist[key >> shift & 255], by_mass ? fixed(weight(x)) : 1ull);
+      if (key >= edge && (key & mask) == prefix) {
+        const Mass m = by_mass ? Mass::of(weight(x)) : Mass{1, 0};
+        atomicAdd(&sm.hist.sum[key >> shift & 255], m.sum);
+        if (m.low) atomicAdd(&sm.hist.low[key >> shift & 255], m.low);
+      }
     }
     __syncthreads();
     if (tid == 0) {
-      u64 c = before, at = before;
+      Mass c = before, at = before;
       int pick = -1;
       for (int d = 255; d >= 0; --d) {
-        if (!sm.hist[d]) continue;
+        const Mass m = {sm.hist.sum[d], sm.hist.low[d]};
+        if (!m.any()) continue;
         // the last digit that starts below the goal (the first one always does or is taken)
-        if (pick >= 0 && !(by_mass ? (double)c < goal : c < (u64)top_k)) break;
+        if (pick >= 0 && !(c.value() < goal)) break;
         pick = d;
         at = c;
-        c += sm.hist[d];
+        c.add(m);
       }
       sm.digit = pick;
-      sm.before = at;
+      sm.before = at.sum;
+      sm.before_low = at.low;
     }
     __syncthreads();
-    before = sm.before;
+    before = {sm.before, sm.before_low};
     prefix |= sm.digit << shift;
     mask |= 255u << shift;
   }
   if (!by_mass) {
     edge = prefix;
-    n_edge = top_k - (int)before;
+    n_edge = top_k - (int)before.sum;
     return;
   }
   // equals at the border: kept while the mass before them is below the goal
-  const u64 w = fixed(weight(value_of(prefix)));
+  const double w = weight(value_of(prefix)) * kScale;
   const int most = prefix == edge ? n_edge : row.V;
   int n = 1;
-  if (w) {
-    const double d = (goal - (double)before) / (double)w;
+  if (w > 0.0) {
+    const double d = (goal - before.value()) / w;
     n = d >= (double)most ? most : max(1, (int)ceil(d));
   }
   edge = prefix;

@@ -105,6 +105,49 @@ def test_bf16_magnitudes(scale, shift):
     compare(x, u, top_k=np.full(R, 2000, np.int32), top_p=np.full(R, 0.7, np.float32))
 
 
+def kept_of_top_p(x, k, p):
+    """Mask of the tokens that top-k and top-p keep, sums in 64-bit mantissas."""
+    w = np.exp(x.astype(np.longdouble) - x.max())
+    order = np.argsort(-x, kind="stable")[:k]
+    mass = np.cumsum(w[order])
+    kept = np.zeros(len(x), bool)
+    kept[order[mass - w[order] < np.longdouble(p) * mass[-1]]] = True
+    return kept, w
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("spread", [0.0, 2.0])
+@pytest.mark.parametrize("by_k", [True, False])
+@pytest.mark.parametrize("rows", [1, 160])
+def test_top_p_next_to_one(dtype, spread, by_k, rows):
+    """A million weights around e^-30 behind one of 1: half of them lie below top_p's border, and
+    tokens on either side of what they add up to are told apart."""
+    V, p = 1 << 20, np.float32(1 - 2.0 ** -24)
+    g = np.random.default_rng(33)
+    x = torch.from_numpy((-30 - spread * (g.random(V) - 0.5)).astype(np.float32))
+    x[-1] = 0.0
+    x = x.to(dtype)
+    k = V - 1 if by_k else V
+    kept, w = kept_of_top_p(x.float().numpy().astype(np.float64), k, p)
+    assert 0.2 * V < kept.sum() < 0.8 * V
+    c = np.cumsum(np.where(kept, w, 0))
+    share = float((c[-1] - 1) / c[-1])
+    u = np.resize(np.float32([0.0, 0.01 * share, 0.3 * share, 0.99 * share, 1.01 * share]), rows)
+    if rows == 1:
+        u[0] = np.float32(0.99 * share)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    ws = L.new_workspace(L.make_sample_problem(rows, V, in_dtype=dtype))
+    xs = x.cuda()[None].expand(rows, V).contiguous()
+    token, lp = L.sample(xs, dev(u), top_p=dev(np.full(rows, p)), workspace=ws,
+                         top_k=dev(np.full(rows, k, np.int32)) if by_k else None)
+    assert L.get_status(ws) == 0
+    want = [int(np.nonzero((c > np.longdouble(v) * c[-1]) & kept)[0][0]) for v in u]
+    got = token.cpu().numpy()
+    # the sums' order leaves the border and the token open by a few thousandths of a token
+    assert np.array_equal(got, want), (got[:5], want[:5])
+    assert np.all(np.abs(lp.cpu().numpy() - np.log((w[want] / c[-1]).astype(float))) <= 2.0 ** -24 * 32)
+
+
 def test_ends_of_the_parameters():
     R, V = 12, 333
     x = logits(R, V, 14)
