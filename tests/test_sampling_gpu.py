@@ -199,6 +199,114 @@ def test_strided_rows(dtype, start, pad):
     compare(x, np.random.default_rng(17).random(R), **mixed(R, 18))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [12, 160])
+@pytest.mark.parametrize("V", [400, 5000, 60_000])
+def test_large_top_k(dtype, rows, V):
+    """top_k of 257 and more: the border by counts through the bits, then top-p's among what is left."""
+    x, u = logits(rows, V, V + 40, dtype), np.random.default_rng(41).random(rows)
+    g = np.random.default_rng(42)
+    k = g.integers(257, V, rows).astype(np.int32)
+    k[:2] = 257, V - 1
+    p = g.random(rows).astype(np.float32)
+    compare(x, u, top_k=k)
+    compare(x, u, top_k=k, top_p=p)
+    compare(x, u, top_k=k, min_p=(0.2 * p).astype(np.float32),
+            temperature=(0.3 + 1.5 * p).astype(np.float32))
+    compare((x * 2).round() / 2, u, top_k=k, top_p=p)
+    compare(-x.abs(), u, top_k=k, top_p=p)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [8, 160])
+def test_small_top_k_among_many_equals(dtype, rows):
+    """More than a thousand logits reach the bound that the stripes give a top_k of up to 256."""
+    V = 6000
+    x = (logits(rows, V, 43) / 2).round().to(dtype)        # some 2300 zeros, 1500 ones
+    u = np.random.default_rng(44).random(rows)
+    for k in (2, 100, 256):
+        k = np.full(rows, k, np.int32)
+        compare(x, u, top_k=k)
+        compare(x, u, top_k=k, top_p=np.full(rows, 0.6, np.float32))
+    z = torch.zeros_like(x)
+    z[:, 5000:] = -1.0
+    compare(z, u, top_k=np.full(rows, 200, np.int32), top_p=np.full(rows, 0.37, np.float32))
+
+
+# more rows than SMs: 512 threads to a row
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [1, 33, 1000, 4097, 50257, 200_003])
+def test_many_rows(dtype, V):
+    R = 160
+    x, u = logits(R, V, V + 50, dtype), np.random.default_rng(V).random(R)
+    compare(x, u)
+    compare(x, u, **mixed(R, V + 51))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_masked_rows(dtype):
+    R, V = 160, 5003
+    x = logits(R, V, 52, dtype)
+    low = torch.finfo(dtype).min
+    x[0::10] = -math.inf
+    x[1::10] = -math.inf
+    x[1::10, 4077] = -3.0
+    x[2::10, ::2] = -math.inf
+    x[3::10, 1::2] = math.nan
+    x[4::10] = math.nan
+    x[5::10, [3, 4200]] = math.inf
+    x[6::10, 1:] = -math.inf
+    x[7::10, :-1] = -math.inf
+    x[8::10] = low
+    x[9::10, :4990] = low
+    for s in range(2):
+        u = np.random.default_rng(s).random(R)
+        got = compare(x, u)
+        assert (got[0::10] == -1).all() and (got[1::10] == 4077).all() and (got[4::10] == -1).all()
+        compare(x, u, **mixed(R, s + 53))
+        compare(x, u, top_k=np.full(R, 2000, np.int32), top_p=np.full(R, 0.9, np.float32))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_rows_at_the_ends_of_the_parameters(dtype):
+    R, V = 160, 2333
+    x = logits(R, V, 54, dtype)
+    u = np.linspace(0, 1, R)
+    one = lambda v, t=np.float32: np.full(R, v, t)
+    for p in ({"top_p": one(0.0)}, {"top_p": one(1 - 2.0 ** -24)}, {"top_p": one(1e-30)},
+              {"min_p": one(1.0)}, {"min_p": one(1e-30)}, {"top_k": one(1, np.int32)},
+              {"top_k": one(V - 1, np.int32)}, {"temperature": one(1e-30)},
+              {"temperature": one(1e30)}, {"temperature": one(3e38), "top_p": one(0.5)}):
+        compare(x, u, **p)
+
+
+@pytest.mark.parametrize("scale,shift", [(0.01, 0.0), (6.0, 3.0), (80.0, 0.0), (3.0, 300.0),
+                                         (3.0, -300.0)])
+def test_many_rows_of_bf16_magnitudes(scale, shift):
+    R, V = 160, 9001
+    x = (logits(R, V, 55, scale=scale) + shift).to(BF16)
+    x[::2, ::7] = 0.0
+    x[1::4, ::5] = -math.inf
+    u = np.random.default_rng(56).random(R)
+    compare(x, u, **mixed(R, 57))
+    compare(x, u, top_p=np.linspace(0.02, 0.9999, R).astype(np.float32))
+    compare(x.float(), u, top_p=np.linspace(0.02, 0.9999, R).astype(np.float32))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("start,pad", [(1, 2), (5, 64)])
+def test_many_strided_rows(dtype, start, pad):
+    R, V = 160, 9001
+    wide = torch.full((R, start + V + pad), math.nan, dtype=dtype, device="cuda")
+    wide[:, :start] = math.inf
+    wide[:, start + V:] = math.inf
+    x = wide[:, start:start + V]
+    x.copy_(logits(R, V, 58, dtype))
+    compare(x, np.random.default_rng(59).random(R), **mixed(R, 60))
+
+
 def test_bad_parameters_leave_the_row():
     R, V = 8, 100
     x = logits(R, V, 19)
