@@ -262,9 +262,12 @@ TV_API tv_status tv_snapshot_commit(const tv_problem *p, const float *snapshots,
  * A decode loop is  tv_prefill (the prompt's state), then per step  tv_tree_verify,  the
  * model's logits,  tv_sample (one target token per node),  tv_tree_accept  and
  * tv_tree_commit;  tv_decode_step  takes the place of a tree for sequences without a draft.
- * The conventions above hold.  The recurrence is fp32 throughout: the states that these
- * entry points write are within 1e-6 of the exact ones (relative, 2-norm), and out is rounded
- * once to its type.  A decay of zero (log_a = -inf, or so low that exp(log_a) is 0 in fp32)
+ * The conventions above hold.  The recurrence has the precision of fp32 throughout: a token adds
+ * roundings of at most some 9 * 2^-24 of the state's norm, of either sign, so a state that
+ * remembers n tokens (until their decay, or the writes over them, leave e^-2) is within
+ * 9 sqrt(n) 2^-24 of the exact one (relative, 2-norm): 5e-6 for 100 tokens, 3e-5 for 4000 without
+ * any decay.  Measured: 1e-6 and less for usual gates, 5e-6 for 4000 tokens of one key without
+ * decay.  out is rounded once to its type.  A decay of zero (log_a = -inf, or so low that exp(log_a) is 0 in fp32)
  * starts a state afresh: at the first token of a call whatever the state given holds, NaN and
  * infinities too; at later tokens of a prompt, from a finite state. */
 

@@ -237,6 +237,26 @@ def test_values(what):
         compare(d, lens, "gdn", run_prefill(d, lens, "gdn", kernel, F32))
 
 
+@pytest.mark.parametrize("mode", ["gdn", "scalar"])
+@pytest.mark.parametrize("repeated", [False, True])
+def test_long_memory(mode, repeated):
+    """4000 tokens without decay (of one key, b = 1): roundings of all of them add up, so the bound is
+    tol's with n = 4000 tokens in place of 100."""
+    T = 4000
+    d = inputs([T], 2, 128, 128, seed=73, mode=mode)
+    d["log_a"].zero_()
+    if repeated:
+        d["k"][:] = d["k"][:1]
+        if mode == "gdn":
+            d["b"].fill_(1.0)
+    want = recurrence(d, [T], mode)
+    bound = 9 * math.sqrt(T) * 2.0 ** -24
+    for kernel in ("tc", "simt"):
+        o, S = run_prefill(d, [T], mode, kernel, F32)
+        check(S, want[1], bound, "state")
+        check(o, want[0], bound + 5 * 2.0 ** -24, "out")
+
+
 @pytest.mark.parametrize("kernel", ["tc", "simt"])
 @pytest.mark.parametrize("mode", ["gdn", "scalar"])
 @pytest.mark.parametrize("value", [-math.inf, -1e30, -3000.0, -80.0])
