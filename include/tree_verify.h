@@ -269,7 +269,12 @@ TV_API tv_status tv_snapshot_commit(const tv_problem *p, const float *snapshots,
  * any decay.  Measured: 1e-6 and less for usual gates, 5e-6 for 4000 tokens of one key without
  * decay.  out is rounded once to its type.  A decay of zero (log_a = -inf, or so low that exp(log_a) is 0 in fp32)
  * starts a state afresh: at the first token of a call whatever the state given holds, NaN and
- * infinities too; at later tokens of a prompt, from a finite state. */
+ * infinities too; at later tokens of a prompt, from a finite state.
+ *   What is given for a token has to be finite (log_a may be -inf).  What is not spoils out and the
+ * state of its head (of every head that shares it, for k) from its token on, q its own token's out
+ * alone; the tensor-core kernel takes 64 tokens together, counted from the sequence's first, and may
+ * spoil those before it among them too.  Other heads, other sequences and earlier tokens are as if it
+ * were not there. */
 
 /* The recurrence over whole prompts: for every token t of a sequence, in order,
  *   S_t as above from S_{t-1},  out_t = S_t q_t,

@@ -353,6 +353,35 @@ def test_nothing_else_is_written(kernel):
     assert L.get_status(ws) == L.binding.TV_ERR_BAD_TREE
 
 
+@pytest.mark.parametrize("kernel", ["tc", "simt"])
+@pytest.mark.parametrize("mode", ["gdn", "scalar"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "log_a", "b"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_token_that_is_not_finite(kernel, mode, name, bad):
+    """It spoils its own sequence and heads, from its token (by chunks: its chunk) on."""
+    if name == "b" and mode == "scalar":
+        pytest.skip("scalar decay has no b")
+    lens, at = [200, 70], 100
+    d = inputs(lens, 4, 128, 128, Hk=2, seed=61, mode=mode)
+    want = run_prefill(d, lens, mode, kernel, F32)
+    d[name] = d[name].clone()
+    d[name][at, 1] = bad
+    o, S = run_prefill(d, lens, mode, kernel, F32)
+    heads = [2, 3] if name in ("q", "k") else [1]
+    others = [h for h in range(4) if h not in heads]
+    first = at // 64 * 64 if kernel == "tc" else at
+    assert torch.equal(o[200:], want[0][200:]) and torch.equal(S[1], want[1][1])
+    assert torch.equal(o[:, others], want[0][:, others])
+    assert torch.equal(S[0, others], want[1][0, others])
+    assert torch.equal(o[:first], want[0][:first])
+    assert not torch.isfinite(o[at, heads]).any()
+    if name == "q":
+        assert torch.equal(o[:at], want[0][:at]) and torch.equal(o[at + 1:], want[0][at + 1:])
+        assert torch.equal(S, want[1])
+    else:
+        assert not torch.isfinite(S[0, heads]).all(-1).all(-1).any()
+
+
 def test_empty_calls():
     d = inputs([0, 0], 2, 128, 128, seed=3)
     o, S = L.prefill(d["q"], d["k"], d["v"], d["log_a"], d["b"], d["offsets"], d["S"], max_len=0)
