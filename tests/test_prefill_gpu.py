@@ -355,6 +355,46 @@ def test_nothing_else_is_written(kernel):
 
 @pytest.mark.parametrize("kernel", ["tc", "simt"])
 @pytest.mark.parametrize("mode", ["gdn", "scalar"])
+@pytest.mark.parametrize("offsets,max_len,good", [
+    ([0, 65, 300, 95], 65, [0]),            # past the rows; the third starts behind its end
+    ([0, 65, 300, 95], 128, [0]),
+    ([0, 40, 20, 20], 65, [0]),             # ends before it starts; an end before the first's
+    ([-1, 40, 40, 40], 65, [1, 2]),
+    ([0, 66, 66, 66], 65, [1, 2]),          # longer than max_len
+    ([0, 66, 100, 128], 65, [1, 2]),
+    ([30, 30, 95, 129], 128, [0, 1]),       # rows before the first, one row too many
+    ([128, 128, 128, 128], 1, [0, 1, 2]),
+    ([0, 2 ** 31 - 1, -2 ** 31, 5], 128, [])])
+def test_good_sequences_beside_bad_ones(kernel, mode, offsets, max_len, good):
+    """Every sequence that the offsets define is computed; nothing else is written."""
+    H, T = 2, 128
+    d = inputs([T], H, 128, 128, seed=79, mode=mode)
+    d["S"] = 0.02 * torch.randn(3, H, 128, 128, device="cuda",
+                                generator=torch.Generator("cuda").manual_seed(79))
+    d["offsets"] = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    out = torch.full((T, H, 128), math.nan, device="cuda")
+    S = torch.full((3, H, 128, 128), math.nan, device="cuda")
+    ws = L.new_workspace(L.make_sequence_problem(3, H, 128, 128, T, max_len, mode, kernel=kernel))
+    L.prefill(d["q"], d["k"], d["v"], d["log_a"], d["b"], d["offsets"], d["S"], max_len=max_len,
+              mode=mode, out=out, S_out=S, kernel=kernel, workspace=ws)
+    assert L.get_status(ws) == (0 if len(good) == 3 else L.binding.TV_ERR_BAD_TREE)
+    rows = torch.zeros(T, dtype=torch.bool, device="cuda")
+    for s in range(3):
+        if s not in good:
+            assert torch.isnan(S[s]).all()
+            continue
+        lo, hi = offsets[s], offsets[s + 1]
+        rows[lo:hi] = True
+        e = {n: None if d[n] is None else d[n][lo:hi] for n in ("q", "k", "v", "log_a", "b")}
+        e.update(offsets=torch.tensor([0, hi - lo]), S=d["S"][s:s + 1])
+        o, Sw = recurrence(e, [hi - lo], mode)
+        check(S[s:s + 1], Sw, tol(hi - lo), "state")
+        check(out[lo:hi], o, tol(hi - lo, F32), "out")
+    assert torch.isnan(out[~rows]).all()
+
+
+@pytest.mark.parametrize("kernel", ["tc", "simt"])
+@pytest.mark.parametrize("mode", ["gdn", "scalar"])
 @pytest.mark.parametrize("name", ["q", "k", "v", "log_a", "b"])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_a_token_that_is_not_finite(kernel, mode, name, bad):
