@@ -61,19 +61,29 @@ def _library() -> ctypes.CDLL:
     return _lib
 
 
+def _int32(*values):
+    """The values, whole; ctypes would cut them to 32 bits without a word."""
+    whole = [int(x) for x in values]
+    if whole and (max(whole) > 0x7fffffff or min(whole) < -0x80000000):
+        raise ValueError(f"a size or bound is beyond 32 bits: {whole}")
+    return whole
+
+
 @functools.lru_cache(maxsize=256)
 def _sequence_problem(*fields) -> SequenceProblem:
-    return SequenceProblem(*fields)
+    return SequenceProblem(*_int32(*fields))
 
 
 def make_sequence_problem(B, H, dk, dv, total_tokens, max_len, mode="gdn", in_dtype=_BF16,
                           out_dtype=None, kernel="auto", qk_heads=0) -> SequenceProblem:
     """``max_len``: upper bound on any sequence's length; ``qk_heads``: 0 = H."""
-    return SequenceProblem(B, H, dk, dv, total_tokens, max_len, 1, MODE[mode], DTYPE[in_dtype],
-                           DTYPE[out_dtype or in_dtype], KERNEL[kernel], 0, qk_heads)
+    return SequenceProblem(*_int32(B, H, dk, dv, total_tokens, max_len, 1, MODE[mode],
+                                   DTYPE[in_dtype], DTYPE[out_dtype or in_dtype], KERNEL[kernel],
+                                   0, qk_heads))
 
 
 def make_sample_problem(rows, vocab, row_stride=None, in_dtype=_F32) -> SampleProblem:
+    rows, vocab = _int32(rows, vocab)
     return SampleProblem(rows, vocab, vocab if row_stride is None else row_stride,
                          DTYPE[in_dtype], 0)
 
@@ -248,6 +258,8 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
         raise TypeError(f"logits has dtype {logits.dtype}, expected {tuple(DTYPE)}")
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("the values of a row of logits must be adjacent")
+    if R > 0x7fffffff or V > 0x7fffffff:
+        raise ValueError(f"logits have shape {tuple(logits.shape)}, beyond 32 bits")
     dev = logits.device
     at = dev.index
     prob = SampleProblem(R, V, logits.stride(0) if R > 1 else V, DTYPE[logits.dtype], 0)
@@ -270,7 +282,7 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
 
 @functools.lru_cache(maxsize=256)
 def _tree_problem(B, T, max_nodes, max_path) -> Problem:
-    return make_problem(B, 1, 16, 16, T, max_nodes, max_path)
+    return make_problem(*_int32(B, 1, 16, 16, T, max_nodes, max_path))
 
 
 @_on_stream

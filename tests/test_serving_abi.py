@@ -146,6 +146,21 @@ def test_binding_refuses_host_tensors():
         L.tree_accept(i, i, i, i, i, max_nodes=4, max_path=2)
 
 
+@pytest.mark.parametrize("i", range(6))
+def test_sizes_beyond_32_bits_are_refused(i):
+    """Not cut to their low 32 bits, which would be a valid size here."""
+    args = [4, 2, 128, 128, 64, 40]
+    args[i] += 1 << 32
+    with pytest.raises(ValueError):
+        L.make_sequence_problem(*args)
+    with pytest.raises(ValueError):
+        serving._sequence_problem(*args, 1, 0, 1, 1, 0, 0, 2)
+    with pytest.raises(ValueError):
+        serving._tree_problem(*[n + (1 << 32) * (i % 4 == j) for j, n in enumerate((4, 64, 16, 4))])
+    with pytest.raises(ValueError):
+        L.make_sample_problem(*[n + (1 << 32) * (i % 2 == j) for j, n in enumerate((3, 100))])
+
+
 # ---- the oracle itself ---------------------------------------------------------------------
 
 
