@@ -7,13 +7,13 @@
 // token is the first in vocabulary order whose cumulated kept weight exceeds u times the total.
 // t = 0 keeps the largest logit alone.
 //
-// Weights and the sums that decide a token are in 64 bits: a token is decided by where u * total
-// falls between two of up to a million borders, and 32-bit weights (1e-7 each) would put
-// one draw in some thousands on the wrong side.  The exponential is the cost (ten 64-bit
+// Weights (to 2e-13 of themselves) and the sums that decide a token are in 64 bits: a token is
+// decided by where u * total falls between two of up to a million borders, and 32-bit weights (1e-7
+// each) would put one draw in some thousands on the wrong side.  The exponential is the cost (ten 64-bit
 // operations, half rate), so each row takes the way with the fewest of them:
 //   t = 0          the largest logit: one read of the row, no weight.
 //   small top-k    every thread keeps the largest logit of its stripe.  The k-th largest of
-//                  these 512 is at most the k-th largest logit, so the few logits above it hold
+//                  these 512 or 1024 is at most the k-th largest logit, so the few logits above it hold
 //                  the prefix; only threads whose own maximum reaches it read their stripe
 //                  again.  What is left is a list of k to a few k tokens in shared memory.
 //   top-p          a second read sums all weights and counts tokens into 2048 bins of the
@@ -33,7 +33,9 @@
 // top-k of 50 114 us, no filter 208 us, top-p 308 us), 128 rows of 100003 in fp32 105 us, one of 32768
 // with top-p 25 to 50 us by temperature and top_p: instructions and the barriers between a row's steps bound it, not bytes.
 // The segment that holds the token is then read once more.  Where a list overflows or top-k is
-// large, the border comes from a radix descent over the logits' bits (slow and general).
+// large, the border comes from a radix descent over the logits' bits, general and slow: its atomics
+// meet in a few of 256 counters (top-k of 1000: 1.2 ms for one row of 32768, 3.6 ms for the 128 rows,
+// 19 ms for the 2048; with top-p 7% more).
 // Second and later reads hit L2.
 #include <math_constants.h>
 
@@ -79,10 +81,10 @@ struct SampleSmem {
   u64 list[kList], sorted[kList];
   double part[kMaxWarps];
   int ipart[kMaxWarps];
-  u64 upart[kMaxWarps], upart_low[kMaxWarps];
-  int n, pick, ties_left, around[2];
+  int n, pick, ties_left, equals, around[2];
   uint32_t digit;
-  u64 before, before_low;
+  u64 before[2];                               // a Mass
+  double goal;
 };
 
 // A sum of weights (of at most 1) as two integers, in steps of 2^-42 and of 2^-84, whose order in the atomics
@@ -95,7 +97,6 @@ struct Mass {
     return {(u64)whole, (u64)__double2ll_rn((x - whole) * kScale)};
   }
   __device__ __forceinline__ void add(Mass o) { sum += o.sum; low += o.low; }
-  __device__ __forceinline__ bool any() const { return sum || low; }
   __device__ __forceinline__ double value() const { return (double)sum + (double)low / kScale; }   // times 2^42
 };
 
@@ -359,39 +360,16 @@ __device__ void filled_around(SampleSmem &sm, int &before, int &after) {
 }
 
 // Border of top-k (by count) or of top-p (by mass) through the bits of the keys, eight at a time.
-// General and slow: up to five reads of the row.
+// General and slow: four reads of the row.  sm.equals is the number of logits at top-k's border.
 template <int kThreads, typename T>
 __device__ void descend(const Row<T> &row, const Weigher &weight, SampleSmem &sm, bool by_mass,
                         int top_k, float top_p, uint32_t &edge, int &n_edge) {
-  constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x;
-  double goal = (double)top_k;
-  if (by_mass) {
-    Mass mass = {0, 0};
-    for (int i = tid; i < row.V; i += kThreads) {
-      const float x = fmaxf(to_f32(row.x[i]), -CUDART_INF_F);
-      if (key_of(x) > edge) mass.add(Mass::of(weight(x)));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-      mass.add({__shfl_xor_sync(kFull, mass.sum, o), __shfl_xor_sync(kFull, mass.low, o)});
-    __syncthreads();
-    if ((tid & 31) == 0) {
-      sm.upart[tid >> 5] = mass.sum;
-      sm.upart_low[tid >> 5] = mass.low;
-    }
-    __syncthreads();
-    mass = edge ? Mass::of(weight(value_of(edge))) : Mass{0, 0};
-    mass.sum *= n_edge;
-    mass.low *= n_edge;
-    for (int w = 0; w < kWarps; ++w) mass.add({sm.upart[w], sm.upart_low[w]});
-    goal = (double)top_p * mass.value();
-  }
   uint32_t prefix = 0, mask = 0;
-  Mass before = {0, 0};
   for (int shift = 24; shift >= 0; shift -= 8) {
     __syncthreads();
     if (tid < 256) sm.hist.sum[tid] = sm.hist.low[tid] = 0;
+    if (tid < 2 && shift == 24) sm.before[tid] = 0;      // (a descent before this one has been read)
     __syncthreads();
     for (int i = tid; i < row.V; i += kThreads) {
       const float x = fmaxf(to_f32(row.x[i]), -CUDART_INF_F);
@@ -404,29 +382,38 @@ __device__ void descend(const Row<T> &row, const Weigher &weight, SampleSmem &sm
     }
     __syncthreads();
     if (tid == 0) {
-      Mass c = before, at = before;
+      if (shift == 24) {
+        // the first read has all the mass; of the equals at top-k's border only n_edge count
+        Mass all = {0, 0};
+        for (int d = 0; d < 256; ++d) all.add({sm.hist.sum[d], sm.hist.low[d]});
+        const Mass e = Mass::of(edge ? weight(value_of(edge)) : 0.0);
+        const u64 out = edge ? sm.equals - n_edge : 0;
+        sm.goal = by_mass ? (double)top_p * Mass{all.sum - out * e.sum, all.low - out * e.low}.value()
+                          : (double)top_k;
+      }
+      Mass c = {sm.before[0], sm.before[1]}, at = c;
       int pick = -1;
       for (int d = 255; d >= 0; --d) {
         const Mass m = {sm.hist.sum[d], sm.hist.low[d]};
-        if (!m.any()) continue;
+        if (!(m.sum || m.low)) continue;
         // the last digit that starts below the goal (the first one always does or is taken)
-        if (pick >= 0 && !(c.value() < goal)) break;
+        if (pick >= 0 && !(c.value() < sm.goal)) break;
         pick = d;
         at = c;
         c.add(m);
       }
       sm.digit = pick;
-      sm.before = at.sum;
-      sm.before_low = at.low;
+      sm.before[0] = at.sum;
+      sm.before[1] = at.low;
+      if (!by_mass) sm.equals = (int)(c.sum - at.sum);
     }
     __syncthreads();
-    before = {sm.before, sm.before_low};
     prefix |= sm.digit << shift;
     mask |= 255u << shift;
   }
   if (!by_mass) {
     edge = prefix;
-    n_edge = top_k - (int)before.sum;
+    n_edge = top_k - (int)sm.before[0];
     return;
   }
   // equals at the border: kept while the mass before them is below the goal
@@ -434,7 +421,7 @@ __device__ void descend(const Row<T> &row, const Weigher &weight, SampleSmem &sm
   const int most = prefix == edge ? n_edge : row.V;
   int n = 1;
   if (w > 0.0) {
-    const double d = (goal - before.value()) / w;
+    const double d = (sm.goal - Mass{sm.before[0], sm.before[1]}.value()) / w;
     n = d >= (double)most ? most : max(1, (int)ceil(d));
   }
   edge = prefix;
