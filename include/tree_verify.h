@@ -285,7 +285,8 @@ TV_API tv_status tv_snapshot_commit(const tv_problem *p, const float *snapshots,
  *   q, k       [T][Hk][dk] in_dtype; v [T][H][dv] in_dtype; log_a, b [T][H] fp32 (b may be
  *              NULL in scalar mode)                                    (device, read)
  *   seq_offsets [B+1] int32: sequence s owns rows seq_offsets[s] .. seq_offsets[s+1]-1.  The
- *              last may end before T: rows that no sequence owns are neither read nor written.
+ *              last may end before T: rows that no sequence owns are not written, and what they
+ *              hold does not matter.
  *              An empty sequence keeps its state                       (device, read)
  *   S_in       [B][H][dv][dk] fp32, or NULL for zero states             (device, read)
  *   out        [T][H][dv] out_dtype; must not overlap any input         (device, written)
@@ -306,8 +307,8 @@ TV_API tv_status tv_prefill(const tv_problem *p, const void *q, const void *k, c
 
 /* The recurrence for one token of every sequence: row s of q, k [B][Hk][dk], v, out [B][H][dv],
  * log_a, b [B][H] belongs to sequence s (p->total_nodes = B).  S_new [B][H][dv][dk] may be S
- * itself, must not partially overlap it.  Nothing in the data can be invalid, so there is no
- * workspace. */
+ * itself, must not partially overlap it; out must not overlap any input.  Nothing in the data can
+ * be invalid, so there is no workspace. */
 TV_API tv_status tv_decode_step(const tv_problem *p, const void *q, const void *k, const void *v,
                                 const float *log_a, const float *b, const float *S, void *out,
                                 float *S_new, tv_stream_t stream);
@@ -328,7 +329,8 @@ typedef struct {
  *           (1: all);
  *   min_p   the tokens that weigh at least min_p (the largest weighs 1; 0: all).
  * The token is the first in vocabulary order whose cumulated kept weight exceeds uniform
- * times the kept total; weights and sums are in 64 bits.
+ * times the kept total.  Weights are to 2e-13 of themselves (one below 2^-1000 is zero), their sums
+ * in 64 bits.
  *   logits      elements need only their own alignment                     (device, read)
  *   uniform     [rows] fp32 in [0, 1], the random numbers                   (device, read)
  *   temperature [rows] fp32, finite, >= 0 (0: the largest logit's token); NULL: 1

@@ -39,10 +39,10 @@ bool prefill_tc_takes(const tv_problem *p) {
          (p->total_nodes / 64 + (long long)p->B) * p->H <= 0x7fffffffLL;
 }
 // Token by token costs 0.21 us a token, or 7 ns for each (sequence, head) where those are more; by
-// chunks 20 to 30 us and 3 to 5 us a chunk for each 148 of them.  Measured, us (token by token / by
-// chunks, gated delta rule): 16 heads 23 / 28 at 96 tokens, 43 / 33 at 192; 32 heads 22 / 24 at 64,
-// 31 / 30 at 96; 128 (sequence, head) pairs 18 / 25 at 16 tokens, 32 / 26 at 32; 1024 pairs 122 / 145
-// at 16, 229 / 145 at 32.
+// chunks 30 us and 3 to 5 us a chunk for each 148 of them.  Measured, us with inputs from HBM (token by
+// token / by chunks, gated delta rule): 16 heads 29 / 36 at 96 tokens, 49 / 40 at 192, 64 / 46 at 256;
+// 32 heads 27 / 32 at 64, 37 / 36 at 96; 128 (sequence, head) pairs 25 / 34 at 16 tokens, 39 / 36 at 32;
+// 1024 pairs 135 / 124 at 16, 246 / 126 at 32, 470 / 132 at 64.
 bool prefill_on_tc(const tv_problem *p) {
   if (p->total_nodes == 0 || p->B == 0 || p->kernel == TV_KERNEL_SIMT || !prefill_tc_takes(p)) return false;
   const long long len = p->max_nodes, pairs = (long long)p->B * p->H;

@@ -1,13 +1,15 @@
 // One token of every sequence through the recurrence, the state updated in one pass:
 //     p = S k,  u = b (v - a p)  (scalar decay: u = v),  S' = a S + u k^T,  o = S' q .
 //
-// The rows of S are independent given k and q, and the state is read and written once, so
-// the step is bound by HBM: 2 * dv * dk * 4 bytes per (sequence, head).  Eight lanes hold a
+// The rows of S are independent given k and q, and the state is read and written once:
+// 2 * dv * dk * 4 bytes per (sequence, head), which bounds large batches.  Eight lanes hold a
 // row (NK float4 each, so a warp's load covers four rows in whole 128-byte segments), and
 // each dot product costs three shuffles.  A CTA takes kRows rows of one state, all of its
 // loads in flight before the first product.
-// 32 sequences of 32 heads, dk = dv = 128: 30.0 us for 136 MB (4.5 TB/s, the rate of a plain copy of
-// that size); 128 sequences 81.9 us for 544 MB (6.6 TB/s, all of the measured copy bandwidth).
+// 128 sequences of 32 heads, dk = dv = 128: 82 us for 544 MB (6.6 TB/s, all of the measured copy
+// bandwidth).  32 sequences: 27 us for 136 MB (5.0 TB/s; a plain copy of the states takes 28.7 us): four
+// waves of CTAs, of which the first waits for its loads and the last for its stores, with DRAM at 30% and
+// issue slots at 28% in between since most of the writes stay in L2.
 #include "serving.cuh"
 
 namespace tv {

@@ -11,12 +11,11 @@
 // of L.  T comes by the 16 x 16 diagonal blocks, by substitution in fp32, one warp each, then the
 // blocks below them by products of 16 x 16 blocks: too small for tcgen05 (128 rows) and, as
 // multiply-adds, bound by the registers' fill from shared memory (128 bytes a cycle), so they are
-// warp-level tf32 products of high and low halves (all shared-memory reads of the kernel halved, 67 to
-// 57 us for 2560 items).
+// warp-level tf32 products of high and low halves, which halved all shared-memory reads of the kernel.
 // The kernel runs apart from the chain over chunks, whose SMs it kept busy when both were one: 1 x 8192
-// tokens of 32 heads took 963 us then, 733 us as two kernels.
-// 4096 items (those 8192 tokens) take 72 us: 187 MB at 2.6 TB/s, the shared-memory pipe 76% busy, which
-// bounds it, issue slots 45%.
+// tokens of 32 heads took 963 us then, 671 us as two kernels.
+// 2560 items (5120 tokens of 32 heads) take 51 us, 4096 (those 8192 tokens) 75 us: 187 MB at 2.5 TB/s, the
+// shared-memory pipe 70% busy, which bounds it, issue slots 46%.
 //
 // Every wait is bounded: one that runs out records TV_ERR_TIMEOUT and ends the CTA.
 #include <algorithm>

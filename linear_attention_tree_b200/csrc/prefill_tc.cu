@@ -35,7 +35,7 @@
 // What bounds it is the chain: 8,100 cycles a chunk (4.6 us), of which the three products on it are
 // 2,650 back to back (24 + 24 MMAs of 37 cycles, 12 of 74); the rest is the chain warps' own work on
 // 128 x 128 values of S and 128 x 64 of R and U at half of the issue slots, and the output's products.
-// One prompt of 8192 tokens, 32 heads, has 32 chains of 128 chunks: 595 us here, 72 us in
+// One prompt of 8192 tokens, 32 heads, has 32 chains of 128 chunks: 595 us here, 75 us in
 // prefill_prepare.cu (floor of the bytes: 41 us).  16 ragged prompts of 16384 tokens in all: 505 us with it
 // (floor 72 us), 8 x 1000 tokens of scalar decay, 16 heads: 95 us (floor 23 us).  Sixteen chain warps
 // instead of eight (latency), U~ and S handed over piece by piece and o stored while R T^T is computed
