@@ -7,11 +7,9 @@
 // head).  A token costs the chain u -> S' -> S' k (the next token's dot product, in four running
 // sums, and three shuffles); o = S' q is formed beside it.  Tokens arrive in double-buffered
 // tiles of kTile by cp.async in their own type and are widened as they are read.  fp32 throughout.
-// Bound by that chain where CTAs are few, 0.2 us a token (16 heads, 256 tokens: 51 us; 94 us with the
-// dot product as one running sum before the update), by instructions where they are many (32 x 64
-// tokens, 32 heads: 401 us).
-#include <type_traits>
-
+// Bound by that chain where CTAs are few, 0.2 us a token (16 heads, 256 tokens: 62 us, 2048: 445 us; as
+// one running sum before the update the dot product made it nearly twice that), by instructions where they
+// are many (32 x 64 tokens, 32 heads: 450 us).
 #include "serving.cuh"
 #include "tc_ptx.cuh"
 
@@ -97,7 +95,12 @@ __global__ void __launch_bounds__(kThreads) prefill_kernel(SequenceArgs a) {
     if (threadIdx.x == 0) set_status(a.ws, TV_ERR_BAD_TREE, s);
     return;
   }
-  if (n > 0) fetch<Tin, kGdn>(a, tile[0], lo, min(kTile, n), h, kh, r0);
+  const float *S_in = a.S_in;
+  if (n > 0) {
+    // a first decay of zero starts afresh, also from NaN and infinity
+    if (expf(a.log_a[(size_t)lo * H + h]) == 0.f) S_in = nullptr;
+    fetch<Tin, kGdn>(a, tile[0], lo, min(kTile, n), h, kh, r0);
+  }
 
   const size_t state = (size_t)item * dv * dk + (size_t)(r0 + group) * dk;
   float4 S[NK];
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) prefill_kernel(SequenceArgs a) {
   for (int i = 0; i < NK; ++i) {
     const int col = 4 * (lane8 + 8 * i);
     S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.S_in && col < dk) S[i] = *reinterpret_cast<const float4 *>(a.S_in + state + col);
+    if (S_in && col < dk) S[i] = *reinterpret_cast<const float4 *>(S_in + state + col);
   }
 
   Tout *out = static_cast<Tout *>(a.out);
@@ -116,10 +119,6 @@ __global__ void __launch_bounds__(kThreads) prefill_kernel(SequenceArgs a) {
     if (t0 + kTile < n)
       fetch<Tin, kGdn>(a, tile[buf ^ 1], (size_t)lo + t0 + kTile, min(kTile, n - t0 - kTile), h, kh, r0);
     const Tile<Tin> &tl = tile[buf];
-    // A decay of zero (below exp(-103)) starts afresh, also from NaN and infinity: looked for in a tile, and
-    // in its tokens only where one may have it (in every token: 39.5 us for 219 tokens in fp32, not 34.9).
-    const int mine = min((int)threadIdx.x & (kTile - 1), m - 1);
-    const bool low = __any_sync(0xffffffffu, tl.la[mine] < -103.f);
     const auto load = [&](const Tin *row, float4 (&x)[NK]) {
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
@@ -131,44 +130,33 @@ __global__ void __launch_bounds__(kThreads) prefill_kernel(SequenceArgs a) {
     load(tl.k[0], k);
 #pragma unroll
     for (int i = 0; i < NK; ++i) dot4(S[i], k[i], sp);
-    const auto tokens = [&](auto resets) {
-      float p = kGdn ? sum8(sum4(sp)) : 0.f, decay = expf(tl.la[0]);
-#pragma unroll(decltype(resets)::value ? 1 : 2)
-      for (int t = 0; t < m; ++t) {
-        const int next = min(t + 1, m - 1);
-        float4 q[NK], kn[NK];
-        load(tl.q[t], q);
-        load(tl.k[next], kn);
-        const float decay_next = expf(tl.la[next]);
-        if (decltype(resets)::value && decay == 0.f) {
-          p = 0.f;
+    float p = kGdn ? sum8(sum4(sp)) : 0.f, decay = expf(tl.la[0]);
+#pragma unroll 2
+    for (int t = 0; t < m; ++t) {
+      const int next = min(t + 1, m - 1);
+      float4 q[NK], kn[NK];
+      load(tl.q[t], q);
+      load(tl.k[next], kn);
+      const float decay_next = expf(tl.la[next]);
+      float u = to_f32(tl.v[t][group]);
+      if (kGdn) u = tl.b[t] * (u - decay * p);
+      float4 so = make_float4(0.f, 0.f, 0.f, 0.f);
+      sp = so;
 #pragma unroll
-          for (int i = 0; i < NK; ++i) S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        float u = to_f32(tl.v[t][group]);
-        if (kGdn) u = tl.b[t] * (u - decay * p);
-        float4 so = make_float4(0.f, 0.f, 0.f, 0.f);
-        sp = so;
-#pragma unroll
-        for (int i = 0; i < NK; ++i) {
-          S[i].x = fmaf(u, k[i].x, decay * S[i].x);
-          S[i].y = fmaf(u, k[i].y, decay * S[i].y);
-          S[i].z = fmaf(u, k[i].z, decay * S[i].z);
-          S[i].w = fmaf(u, k[i].w, decay * S[i].w);
-          if (kGdn) dot4(S[i], kn[i], sp);
-          dot4(S[i], q[i], so);
-          k[i] = kn[i];
-        }
-        const float o = sum8(sum4(so));
-        if (kGdn) p = sum8(sum4(sp));
-        decay = decay_next;
-        if (lane8 == 0) o_tile[buf][t][group] = o;
+      for (int i = 0; i < NK; ++i) {
+        S[i].x = fmaf(u, k[i].x, decay * S[i].x);
+        S[i].y = fmaf(u, k[i].y, decay * S[i].y);
+        S[i].z = fmaf(u, k[i].z, decay * S[i].z);
+        S[i].w = fmaf(u, k[i].w, decay * S[i].w);
+        if (kGdn) dot4(S[i], kn[i], sp);
+        dot4(S[i], q[i], so);
+        k[i] = kn[i];
       }
-    };
-    if (low)
-      tokens(std::true_type());
-    else
-      tokens(std::false_type());
+      const float o = sum8(sum4(so));
+      if (kGdn) p = sum8(sum4(sp));
+      decay = decay_next;
+      if (lane8 == 0) o_tile[buf][t][group] = o;
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < m * kRows; e += kThreads)
       out[((size_t)(lo + t0 + e / kRows) * H + h) * dv + r0 + e % kRows] =
