@@ -267,9 +267,9 @@ TV_API tv_status tv_snapshot_commit(const tv_problem *p, const float *snapshots,
  * remembers n tokens (until their decay, or the writes over them, leave e^-2) is within
  * 9 sqrt(n) 2^-24 of the exact one (relative, 2-norm): 5e-6 for 100 tokens, 3e-5 for 4000 without
  * any decay.  Measured: 1e-6 and less for usual gates, 5e-6 for 4000 tokens of one key without
- * decay.  out is rounded once to its type.  A decay of zero (log_a = -inf, or so low that exp(log_a) is 0 in fp32)
- * starts a state afresh: at the first token of a call whatever the state given holds, NaN and
- * infinities too; at later tokens of a prompt, from a finite state.
+ * decay.  out is rounded once to its type.  A decay of zero (log_a = -inf, or so low that
+ * exp(log_a) is 0 in fp32) starts a state afresh: at the first token of a call whatever the state
+ * given holds, NaN and infinities too; at later tokens of a prompt, from a finite state.
  *   What is given for a token has to be finite (log_a may be -inf).  What is not spoils out and the
  * state of its head (of every head that shares it, for k) from its token on, q its own token's out
  * alone; the tensor-core kernel takes 64 tokens together, counted from the sequence's first, and may
